@@ -60,11 +60,18 @@ typedef enum {
     RM_ERR_DEVICE_BOUNDS = 6    /* a device-side bounds check failed            */
 } rm_status;
 
-typedef enum { RM_F32 = 0, RM_BF16 = 1 } rm_dtype;
+/* RM_E4M3 (8 bits, with block scales) names an operand or result of the
+ * block-scaled linear layer only; no handle has it. */
+typedef enum { RM_F32 = 0, RM_BF16 = 1, RM_E4M3 = 2 } rm_dtype;
 
 /* FFN activation: GELU (tanh form or exact erf form), or ReLU (the activation
  * of the Mixer backbone timed in Appendix B of "重新理解 RankMixer"). */
-typedef enum { RM_ACT_GELU_TANH = 0, RM_ACT_GELU_ERF = 1, RM_ACT_RELU = 2 } rm_act;
+typedef enum {
+    RM_ACT_GELU_TANH = 0,
+    RM_ACT_GELU_ERF = 1,
+    RM_ACT_RELU = 2,
+    RM_ACT_NONE = 3     /* rm_matmul_fp8_block only */
+} rm_act;
 
 typedef struct {
     int B_max;       /* largest batch any call will pass                         */
@@ -261,6 +268,148 @@ typedef struct {
 rm_status rm_quantize_fp8(const void *src, void *dst, float *scale, long long rows, int K, rm_stream_t stream);
 rm_status rm_stack_forward_fp8(rm_handle *h, const rm_block_weights *blocks, const rm_fp8_weights *q, const void *X0,
                                float *pooled, int B, rm_stream_t stream);
+
+/* ---- block-scaled 8-bit linear layer ---------------------------------------
+ * RMS norm with an 8-bit output, its gradient, the block quantiser and the
+ * matrix product of the quantised operands: the parts of an FFN (or any linear
+ * layer) whose operands are e4m3 with one scale for each block of 128, for
+ * serving and, with the transposed operands, for training.  The pages have no
+ * counterpart; the scheme is this library's own.
+ *
+ * Block scales.  128 consecutive elements of a row (the last block of a row
+ * may be shorter), or a 128 x 128 square, share a scale 2^e held in one byte,
+ * e + 127 (E8M0; 255 = NaN), with e the smallest integer in [-127, 127] such
+ * that max |x| <= 448 * 2^e, 0 for a block of zeros.  The element is
+ * e4m3(x / 2^e), rounded to nearest even: a power of two adds no rounding of
+ * its own.  A block that holds an infinity or a NaN gets scale byte 255 and
+ * NaN codes, so products with it are NaN rather than finite and wrong.
+ *
+ * Conventions.  No handle and no workspace beyond what a call names: sizes and
+ * strides come with each call, so calls may overlap on any streams as long as
+ * their outputs are disjoint.  Strides are in elements; row strides ("ld") and
+ * group strides make rows and groups that start on 16-byte boundaries (scale
+ * bytes have no such rule), and rows of an array do not overlap.  A stride of
+ * a dimension of size 1 is not used.  The current device is the tensors'.
+ * Nothing is written outside the named [rows][cols] of an output: padding
+ * between rows stays as it was.  Empty problems (no rows, no groups) return
+ * RM_OK without a launch. */
+
+/* RMS norm with residual, row by row over D:
+ *     s = X + R rounded to dtype (s = X when R is NULL)
+ *     r = 1 / sqrt(mean(s^2) + eps)
+ *     y = s * r * gamma            (gamma NULL: 1)
+ * fp32 arithmetic; every output may be NULL, but not all of them:
+ *     Sum [rows][D] dtype: s (may be X or R)     Y [rows][D] dtype: y
+ *     Yq [rows][D] e4m3 and Ys [rows][ceil(D/128)] scale bytes (both or
+ *     neither): y quantised from fp32 in blocks of 128 along the row
+ *     rstd [rows] float: r, which the gradient wants.
+ * D % 16 == 0 and D <= 16384, else RM_ERR_UNSUPPORTED; eps >= 0. */
+typedef struct {
+    const void *X, *R;
+    const float *gamma;
+    void *Sum, *Y, *Yq;
+    unsigned char *Ys;
+    float *rstd;
+    long long ld_x, ld_r, ld_sum, ld_y, ld_yq, ld_ys;   /* row strides */
+    long long rows;
+    int D;
+    rm_dtype dtype;      /* of X, R, Sum, Y: RM_BF16 or RM_F32 */
+    float eps;
+} rm_rmsnorm_args;
+rm_status rm_rmsnorm_forward(const rm_rmsnorm_args *args, rm_stream_t stream);
+
+/* Gradient of rm_rmsnorm_forward: with dY = dL/dy (an 8-bit output passes its
+ * gradient straight through), S and rstd as the forward call left them,
+ *     a = gamma * dY
+ *     dX = rstd * (a - S * rstd^2 * mean(a * S)) + dSum
+ *     dgamma = sum over rows of dY * S * rstd
+ * dX is the gradient of X and of R alike.  dSum (may be NULL) is the gradient
+ * that reaches the residual stream from elsewhere.  dX may be dY or dSum.
+ * dgamma [D] float (may be NULL) is overwritten; it needs `workspace`, device
+ * memory of rm_rmsnorm_backward_workspace_bytes(rows, D) bytes, 16-byte aligned,
+ * which concurrent calls must not share.  Sums are fp32 in a fixed order: equal
+ * calls give equal bits. */
+typedef struct {
+    const void *dY, *S, *dSum;
+    const float *gamma, *rstd;
+    void *dX;
+    float *dgamma;
+    void *workspace;
+    size_t workspace_bytes;
+    long long ld_dy, ld_s, ld_dsum, ld_dx;   /* row strides */
+    long long rows;
+    int D;
+    rm_dtype dtype;      /* of dY, S, dSum, dX: RM_BF16 or RM_F32 */
+} rm_rmsnorm_grad_args;
+size_t rm_rmsnorm_backward_workspace_bytes(long long rows, int D);
+rm_status rm_rmsnorm_backward(const rm_rmsnorm_grad_args *args, rm_stream_t stream);
+
+/* Block quantiser of G matrices src [rows][cols] (bf16 or float), in one read:
+ *     dst [rows][cols] e4m3, scale [ceil(rows/block_rows)][ceil(cols/128)], and / or
+ *     dst_t [cols][rows] e4m3, scale_t [ceil(cols/block_rows)][ceil(rows/128)]:
+ *     the same of the transpose.
+ * block_rows 1: blocks of 1 x 128 along the rows of what is written (of the
+ * transpose for dst_t); 128: squares, whose transpose has the same codes and
+ * scales.  dst_t_ld >= rows is a multiple of 16, rows itself need not be.
+ * cols % 16 == 0, else RM_ERR_UNSUPPORTED. */
+typedef struct {
+    const void *src;
+    long long src_gstride, src_ld;
+    void *dst;
+    long long dst_gstride, dst_ld;
+    unsigned char *scale;
+    long long scale_gstride, scale_ld;
+    void *dst_t;
+    long long dst_t_gstride, dst_t_ld;
+    unsigned char *scale_t;
+    long long scale_t_gstride, scale_t_ld;
+    int G, rows, cols;
+    int block_rows;
+    rm_dtype dtype;      /* of src */
+} rm_quant_block_args;
+rm_status rm_quantize_fp8_block(const rm_quant_block_args *args, rm_stream_t stream);
+
+/* Product of block-scaled operands, group by group:
+ *     out[g][m][n] = act( sum_k A[g][m][k] W[g][n][k] + bias[g][n] ) + resid[g][m][n]
+ * A [G][M][K] e4m3 with scales a_scale [G][M][ceil(K/128)];  W [G][N][K] e4m3
+ * with w_scale [G][ceil(N/w_block_rows)][ceil(K/128)], w_block_rows 1 or 128.
+ * A group stride of 0 shares an input among the groups.  fp32 accumulation in
+ * the tensor cores, every block's scales applied there.
+ * out: out_dtype RM_BF16 or RM_F32 (resid, if given, has the same type and may
+ * be out), or RM_E4M3 with out_scale [G][M][ceil(N/128)] and no resid: the next
+ * product's operand, quantised from fp32.  bias [G][N] float or NULL; act an
+ * rm_act.  N % 16 == 0, else RM_ERR_UNSUPPORTED; any M, K >= 1 (the operands'
+ * row strides are multiples of 16 bytes).
+ * The backward products of out = A W^T are the same call: dA = dOut W with the
+ * transposed weight squares as W, and dW = dOut^T A with both operands
+ * quantised by rm_quantize_fp8_block's transposed form (w_block_rows 1).
+ * wait_budget_ns bounds every device-side wait (0: one second).  device_status
+ * (device pointer to an int that holds RM_OK, may be NULL) becomes
+ * RM_ERR_DEVICE_TIMEOUT if one runs out. */
+typedef struct {
+    const void *A;
+    long long a_gstride, a_ld;
+    const unsigned char *a_scale;
+    long long as_gstride, as_ld;
+    const void *W;
+    long long w_gstride, w_ld;
+    const unsigned char *w_scale;
+    long long ws_gstride, ws_ld;
+    const float *bias;
+    const void *resid;
+    long long r_gstride, r_ld;
+    void *out;
+    long long o_gstride, o_ld;
+    unsigned char *out_scale;
+    long long os_gstride, os_ld;
+    int *device_status;
+    unsigned long long wait_budget_ns;
+    int G, M, N, K;
+    int w_block_rows;
+    int act;             /* rm_act */
+    rm_dtype out_dtype;
+} rm_matmul_fp8_args;
+rm_status rm_matmul_fp8_block(const rm_matmul_fp8_args *args, rm_stream_t stream);
 
 /* ---- token-sharded forward (one rank's share) ------------------------------
  * G ranks each own Tl = T / G consecutive tokens: their rows of every sample

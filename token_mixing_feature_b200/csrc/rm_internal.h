@@ -25,6 +25,11 @@ enum WaitSite : int {
     SITE_LN_POOL = 7,
     SITE_TRAIN_MIX = 8,
     SITE_SELFTEST = 9,
+    SITE_MX_PRODUCER = 10,
+    SITE_MX_SCALES = 11,
+    SITE_MX_MMA = 12,
+    SITE_MX_EPILOGUE = 13,
+    SITE_MX_DRAIN = 14,
 };
 
 // ---- memory-bound kernels (rm_mem.cu); E = 0 float, 1 bf16 -------------
@@ -218,5 +223,48 @@ cudaError_t launch_shard_mix_ln(const void* recv, const void* Xh, const float* g
                                 int B, int Tl, int D, int G, cudaStream_t s);
 cudaError_t launch_shard_pool(const void* V, const void* Sres, const float* g, const float* bt, float eps,
                               float* pooled_part, int B, int Tl, int D, cudaStream_t s);
+
+// ---- block-scaled 8-bit linear layer ------------------------------------------
+// (arguments as in rm_rmsnorm_args, rm_rmsnorm_grad_args, rm_quant_block_args,
+// rm_matmul_fp8_args; strides in elements)
+struct RmsNorm {
+    const void *X, *R;
+    const float* gamma;
+    void *Sum, *Y, *Yq;
+    uint8_t* Ys;
+    float* rstd;
+    long long ld_x, ld_r, ld_sum, ld_y, ld_yq, ld_ys;
+    long long rows;
+    int D;
+    float eps;
+};
+cudaError_t launch_rmsnorm(int dtype, const RmsNorm& p, cudaStream_t s);   // D % 16 == 0, D <= 16384
+struct RmsNormGrad {
+    const void *dY, *S, *dSum;
+    const float *gamma, *rstd;
+    void* dX;
+    float* part;   // [rmsnorm_bwd_parts][D], or null: no dgamma
+    long long ld_dy, ld_s, ld_dsum, ld_dx;
+    long long rows;
+    int D;
+};
+int rmsnorm_bwd_parts(long long rows, int D);
+cudaError_t launch_rmsnorm_bwd(int dtype, const RmsNormGrad& p, float* dgamma, cudaStream_t s);
+struct QuantBlock {
+    const void* src;
+    long long src_gs, src_ld;
+    int G, rows, cols;
+    void* dst;
+    long long dst_gs, dst_ld;
+    uint8_t* scale;
+    long long s_gs, s_ld;
+    void* dst_t;
+    long long dt_gs, dt_ld;
+    uint8_t* scale_t;
+    long long st_gs, st_ld;
+};
+cudaError_t launch_quant_block(int dtype, const QuantBlock& p, int block_rows, cudaStream_t s);
+// out = act(A W^T + bias) + resid, group by group, on block-scaled operands.
+cudaError_t launch_gemm_mx(const rm_matmul_fp8_args& a, int num_sms, cudaStream_t s);
 
 }  // namespace rm

@@ -1,0 +1,113 @@
+// Block-scaled 8-bit values: e4m3 codes with one power-of-two scale (E8M0, a
+// byte holding the exponent + 127; 255 = NaN) for each block of 128, and the
+// sm_100a tensor-core instructions that read both (kind::mxf8f6f4).
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "rm_device.cuh"
+
+namespace rm {
+
+constexpr int kBlk = 128;   // elements that share a scale along a row
+
+// ------------------------------------------------------------------- scales
+// |x| as an integer: ordered like the magnitudes, infinity and NaN on top, so
+// one unsigned maximum finds both the largest magnitude and any NaN.
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// Scale byte of a block whose largest magnitude is `amax` (abs_bits): the
+// smallest e in [-127, 127] with amax <= 448 * 2^e = 1.75 * 2^(e + 8), read off
+// the exponent and mantissa fields; 127 (scale 1) for a zero block, 255 (NaN)
+// for one with an infinity or a NaN.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
+    if (amax >= 0x7f800000u) return 255u;
+    if (amax == 0u) return 127u;
+    const int b = (int)(amax >> 23) - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return (uint32_t)max(b, 0);
+}
+// 2^-e of a scale byte other than 255: e = 127 at most is reached by no finite
+// fp32 block (byte <= 247), so the power is a normal number.
+__device__ __forceinline__ float scale_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+
+// Four e4m3 codes (nearest even; |x * inv| <= 448 by the choice of the scale,
+// the saturation only meets NaN blocks, whose codes the caller replaces).
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+constexpr uint32_t kNanCodes = 0x7f7f7f7fu;
+
+// ------------------------------------------------------------- tensor cores
+// Instruction descriptor of kind::mxf8f6f4: e4m3 A and B (format code 0), both
+// K-major, E8M0 scales; the two scale ids name the byte of each row's 32-bit
+// scale word that the instruction applies.
+__host__ __device__ constexpr uint32_t idesc_mx_e4m3(int M, int N, int a_id, int b_id) {
+    return ((uint32_t)b_id << 4)            // B scale id
+           | ((uint32_t)(N >> 3) << 17)     // N / 8
+           | (1u << 23)                     // scale type: E8M0
+           | ((uint32_t)(M >> 4) << 24)     // M / 16
+           | ((uint32_t)a_id << 29);        // A scale id
+}
+
+// Unswizzled K-major descriptor of a scale atom: 32 rows of 16 bytes.
+__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1u << 16) | ((uint64_t)(128u >> 4) << 32) |
+           ((uint64_t)1u << 46);
+}
+
+// One scale atom (128 rows x one 32-bit word of four K blocks' scales; row r's
+// word at byte (r % 32) * 16 + (r / 32) * 4 of shared memory) into four tensor
+// memory columns, repeated in every 32-lane quarter.
+template <int CG>
+__device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint64_t desc) {
+    if constexpr (CG == 2)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// D[tmem] (+)= (A scaled) (B scaled)^T, K = 32, one scale per row and 32 K.
+template <int CG>
+__device__ __forceinline__ void tc_mma_mx(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t a_scale, uint32_t b_scale, uint32_t accumulate) {
+    if constexpr (CG == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+                d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+                d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate)
+            : "memory");
+}
+
+// The 32-bit word of scales of K blocks [4 chunk, 4 chunk + 4) of one row
+// (scale 1 past the last block); vec: the row starts on a 4-byte boundary.
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int chunk, int blocks, bool vec) {
+    const int n = blocks - 4 * chunk;
+    const uint8_t* p = row + 4 * (long long)chunk;
+    if (vec && n >= 4) return __ldcg(reinterpret_cast<const uint32_t*>(p));
+    uint32_t w = 0x7f7f7f7fu;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < n) w = (w & ~(0xffu << (8 * i))) | ((uint32_t)__ldcg(p + i) << (8 * i));
+    return w;
+}
+
+// ---------------------------------------------------------- wide accesses
+__device__ __forceinline__ void stg256(void* p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+}  // namespace rm

@@ -15,8 +15,8 @@ _LIB_PATH = pathlib.Path(__file__).resolve().with_name("librankmixer.so")
 
 RM_OK, RM_ERR_INVALID_ARG, RM_ERR_UNSUPPORTED, RM_ERR_CUDA, RM_ERR_OOM, \
     RM_ERR_DEVICE_TIMEOUT, RM_ERR_DEVICE_BOUNDS = range(7)
-RM_F32, RM_BF16 = 0, 1
-RM_ACT_GELU_TANH, RM_ACT_GELU_ERF, RM_ACT_RELU = 0, 1, 2
+RM_F32, RM_BF16, RM_E4M3 = 0, 1, 2
+RM_ACT_GELU_TANH, RM_ACT_GELU_ERF, RM_ACT_RELU, RM_ACT_NONE = 0, 1, 2, 3
 DTYPES = {"f32": RM_F32, "bf16": RM_BF16}
 ACTS = {"tanh": RM_ACT_GELU_TANH, "erf": RM_ACT_GELU_ERF, "relu": RM_ACT_RELU}
 
@@ -30,6 +30,8 @@ EXPORTED = (
     "rm_train_create", "rm_train_destroy", "rm_train_workspace_bytes", "rm_train_step", "rm_train_sync_status",
     "rm_train_set_reg", "rm_tokshard_pack", "rm_tokshard_mix_ln", "rm_tokshard_pool",
     "rm_quantize_fp8", "rm_stack_forward_fp8",
+    "rm_rmsnorm_forward", "rm_rmsnorm_backward", "rm_rmsnorm_backward_workspace_bytes", "rm_quantize_fp8_block",
+    "rm_matmul_fp8_block",
 )
 RM_STATIC_SCRATCH_BYTES = 16 << 20
 RM_K_COUNT = 11
@@ -54,6 +56,33 @@ class rm_fp8_weights(ctypes.Structure):
 class rm_block_grads(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("W1", "b1", "W2", "b2", "ln1_g", "ln1_b", "ln2_g", "ln2_b",
                                                 "Wr", "br", "Wr_infer", "br_infer")]
+
+
+def _fields(spec: str):
+    types = {"p": ctypes.c_void_p, "q": ctypes.c_longlong, "i": ctypes.c_int, "f": ctypes.c_float,
+             "z": ctypes.c_size_t, "u": ctypes.c_ulonglong}
+    return [(n, types[t]) for t, names in (part.split(":") for part in spec.split(";")) for n in names.split()]
+
+
+class rm_rmsnorm_args(ctypes.Structure):
+    _fields_ = _fields("p:X R gamma Sum Y Yq Ys rstd;q:ld_x ld_r ld_sum ld_y ld_yq ld_ys rows;i:D dtype;f:eps")
+
+
+class rm_rmsnorm_grad_args(ctypes.Structure):
+    _fields_ = _fields("p:dY S dSum gamma rstd dX dgamma workspace;z:workspace_bytes;"
+                       "q:ld_dy ld_s ld_dsum ld_dx rows;i:D dtype")
+
+
+class rm_quant_block_args(ctypes.Structure):
+    _fields_ = _fields("p:src;q:src_gstride src_ld;p:dst;q:dst_gstride dst_ld;p:scale;q:scale_gstride scale_ld;"
+                       "p:dst_t;q:dst_t_gstride dst_t_ld;p:scale_t;q:scale_t_gstride scale_t_ld;"
+                       "i:G rows cols block_rows dtype")
+
+
+class rm_matmul_fp8_args(ctypes.Structure):
+    _fields_ = _fields("p:A;q:a_gstride a_ld;p:a_scale;q:as_gstride as_ld;p:W;q:w_gstride w_ld;p:w_scale;"
+                       "q:ws_gstride ws_ld;p:bias resid;q:r_gstride r_ld;p:out;q:o_gstride o_ld;p:out_scale;"
+                       "q:os_gstride os_ld;p:device_status;u:wait_budget_ns;i:G M N K w_block_rows act out_dtype")
 
 
 class RankMixerError(RuntimeError):
@@ -105,6 +134,11 @@ def _load() -> ctypes.CDLL:
         "rm_quantize_fp8": (st, [vp, vp, vp, ctypes.c_longlong, ci, vp]),
         "rm_stack_forward_fp8": (st, [vp, ctypes.POINTER(rm_block_weights), ctypes.POINTER(rm_fp8_weights), vp, vp,
                                       ci, vp]),
+        "rm_rmsnorm_forward": (st, [ctypes.POINTER(rm_rmsnorm_args), vp]),
+        "rm_rmsnorm_backward": (st, [ctypes.POINTER(rm_rmsnorm_grad_args), vp]),
+        "rm_rmsnorm_backward_workspace_bytes": (ctypes.c_size_t, [ctypes.c_longlong, ci]),
+        "rm_quantize_fp8_block": (st, [ctypes.POINTER(rm_quant_block_args), vp]),
+        "rm_matmul_fp8_block": (st, [ctypes.POINTER(rm_matmul_fp8_args), vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -408,3 +442,197 @@ def rm_stack_forward_fp8(h: Handle, blocks: Sequence[Dict], qblocks: Sequence[Di
         qarr[i] = rm_fp8_weights(**{n: _ptr(q[n]) for n, _ in rm_fp8_weights._fields_})
     _check(_lib.rm_stack_forward_fp8(h.ptr, arr, qarr, _ptr(X0), _ptr(pooled), B, _stream(stream)),
            "rm_stack_forward_fp8")
+
+
+# --------------------------------------------- block-scaled 8-bit linear layer
+# These take torch tensors (strided views are fine as long as the last dimension
+# is contiguous), read sizes and strides off them and refuse what the C call
+# cannot see: wrong types, shapes or devices.  8-bit tensors are uint8 or
+# float8_e4m3fn, scale bytes uint8 or float8_e8m0fnu.
+_FP8_ACTS = {**ACTS, "none": RM_ACT_NONE, None: RM_ACT_NONE}
+
+
+def _refuse(what: str, why: str):
+    raise RankMixerError(RM_ERR_INVALID_ARG, f"{what}: {why}")
+
+
+def _stream_dtypes():
+    import torch
+    return {torch.bfloat16: RM_BF16, torch.float32: RM_F32}
+
+
+def _need(what: str, device: int, **tensors) -> None:
+    """Every tensor that is given lies on the current device `device`, its last dimension contiguous."""
+    for name, t in tensors.items():
+        if t is not None:
+            if t.get_device() != device:
+                _refuse(what, f"{name} is not on the current CUDA device")
+            if t.stride(-1) != 1 and t.shape[-1] > 1:
+                _refuse(what, f"{name}'s last dimension is not contiguous")
+
+
+def _shape(what: str, name: str, t, shape) -> None:
+    if t is not None and tuple(t.shape) != tuple(shape):
+        _refuse(what, f"{name} has shape {tuple(t.shape)}, wanted {tuple(shape)}")
+
+
+def _bytes8(what: str, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.element_size() != 1:
+            _refuse(what, f"{name} holds no 8-bit values")
+
+
+def _f32(what: str, **tensors) -> None:
+    import torch
+    for name, t in tensors.items():
+        if t is not None and t.dtype != torch.float32:
+            _refuse(what, f"{name} is not float32")
+
+
+def _ld(t, dim: int = 0) -> int:
+    """Stride of a dimension (0 if there is no tensor); the last dimension's extent, rounded up to what every
+    type's 16-byte rows take, where the dimension has one entry and torch's stride means nothing."""
+    if t is None:
+        return 0
+    return t.stride(dim) if t.shape[dim] > 1 else (t.shape[-1] + 15) // 16 * 16
+
+
+def _current_device() -> int:
+    import torch
+    return torch.cuda.current_device()
+
+
+def rm_rmsnorm_forward(X, R=None, gamma=None, Sum=None, Y=None, Yq=None, Ys=None, rstd=None, eps: float = 1e-5,
+                       stream=None) -> None:
+    """s = X + R, y = s / sqrt(mean(s^2) + eps) * gamma for rows X [rows, D]; outputs Sum (s), Y (y), Yq and Ys
+    (y in e4m3 with a scale for each 128), rstd, each of them optional."""
+    what = "rm_rmsnorm_forward"
+    if X.dim() != 2:
+        _refuse(what, "X is not [rows, D]")
+    dt = _stream_dtypes().get(X.dtype)
+    if dt is None:
+        _refuse(what, "X is neither bfloat16 nor float32")
+    rows, D = X.shape
+    _need(what, _current_device(), X=X, R=R, gamma=gamma, Sum=Sum, Y=Y, Yq=Yq, Ys=Ys, rstd=rstd)
+    for name, t in (("R", R), ("Sum", Sum), ("Y", Y)):
+        if t is not None and t.dtype != X.dtype:
+            _refuse(what, f"{name} has another type than X")
+        _shape(what, name, t, (rows, D))
+    _f32(what, gamma=gamma, rstd=rstd)
+    _bytes8(what, Yq=Yq, Ys=Ys)
+    _shape(what, "gamma", gamma, (D,))
+    _shape(what, "rstd", rstd, (rows,))
+    _shape(what, "Yq", Yq, (rows, D))
+    _shape(what, "Ys", Ys, (rows, (D + 127) // 128))
+    a = rm_rmsnorm_args(_ptr(X), _ptr(R), _ptr(gamma), _ptr(Sum), _ptr(Y), _ptr(Yq), _ptr(Ys), _ptr(rstd), _ld(X),
+                        _ld(R), _ld(Sum), _ld(Y), _ld(Yq), _ld(Ys), rows, D, dt, eps)
+    _check(_lib.rm_rmsnorm_forward(ctypes.byref(a), _stream(stream)), what)
+
+
+def rm_rmsnorm_backward_workspace_bytes(rows: int, D: int) -> int:
+    return _lib.rm_rmsnorm_backward_workspace_bytes(rows, D)
+
+
+def rm_rmsnorm_backward(dY, S, gamma, rstd, dSum, dX, dgamma=None, workspace=None, stream=None) -> None:
+    """dX = dL/dX (= dL/dR) and dgamma of rm_rmsnorm_forward from dY = dL/dy, the saved S and rstd, and dSum, the
+    gradient that reaches Sum from elsewhere (or None).  dgamma needs a workspace of
+    rm_rmsnorm_backward_workspace_bytes(rows, D) bytes."""
+    what = "rm_rmsnorm_backward"
+    if S.dim() != 2:
+        _refuse(what, "S is not [rows, D]")
+    dt = _stream_dtypes().get(S.dtype)
+    if dt is None:
+        _refuse(what, "S is neither bfloat16 nor float32")
+    rows, D = S.shape
+    _need(what, _current_device(), dY=dY, S=S, gamma=gamma, rstd=rstd, dSum=dSum, dX=dX, dgamma=dgamma,
+          workspace=workspace)
+    for name, t in (("dY", dY), ("dSum", dSum), ("dX", dX)):
+        if t is not None and t.dtype != S.dtype:
+            _refuse(what, f"{name} has another type than S")
+        _shape(what, name, t, (rows, D))
+    _f32(what, gamma=gamma, rstd=rstd, dgamma=dgamma)
+    _shape(what, "gamma", gamma, (D,))
+    _shape(what, "rstd", rstd, (rows,))
+    _shape(what, "dgamma", dgamma, (D,))
+    if workspace is not None and not workspace.is_contiguous():
+        _refuse(what, "the workspace is not contiguous")
+    a = rm_rmsnorm_grad_args(_ptr(dY), _ptr(S), _ptr(dSum), _ptr(gamma), _ptr(rstd), _ptr(dX), _ptr(dgamma),
+                             _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+                             _ld(dY), _ld(S), _ld(dSum), _ld(dX), rows, D, dt)
+    _check(_lib.rm_rmsnorm_backward(ctypes.byref(a), _stream(stream)), what)
+
+
+def rm_quantize_fp8_block(src, dst=None, scale=None, dst_t=None, scale_t=None, block_rows: int = 1,
+                          stream=None) -> None:
+    """src [rows, cols] or [G, rows, cols] to e4m3 dst (same shape) with scale [.., ceil(rows / block_rows),
+    ceil(cols / 128)], and / or to its transpose dst_t [.., cols, rows] with scale_t [.., ceil(cols / block_rows),
+    ceil(rows / 128)]."""
+    what = "rm_quantize_fp8_block"
+    if src.dim() == 2:
+        src, dst, scale, dst_t, scale_t = (t if t is None else t.unsqueeze(0) for t in (src, dst, scale, dst_t, scale_t))
+    if src.dim() != 3:
+        _refuse(what, "src is neither [rows, cols] nor [G, rows, cols]")
+    dt = _stream_dtypes().get(src.dtype)
+    if dt is None:
+        _refuse(what, "src is neither bfloat16 nor float32")
+    if block_rows not in (1, 128):
+        _refuse(what, "block_rows is neither 1 nor 128")
+    G, rows, cols = src.shape
+    _need(what, _current_device(), src=src, dst=dst, scale=scale, dst_t=dst_t, scale_t=scale_t)
+    _bytes8(what, dst=dst, scale=scale, dst_t=dst_t, scale_t=scale_t)
+    _shape(what, "dst", dst, (G, rows, cols))
+    _shape(what, "scale", scale, (G, -(-rows // block_rows), (cols + 127) // 128))
+    _shape(what, "dst_t", dst_t, (G, cols, rows))
+    _shape(what, "scale_t", scale_t, (G, -(-cols // block_rows), (rows + 127) // 128))
+    a = rm_quant_block_args(_ptr(src), _ld(src, 0), _ld(src, 1), _ptr(dst), _ld(dst, 0), _ld(dst, 1), _ptr(scale),
+                            _ld(scale, 0), _ld(scale, 1), _ptr(dst_t), _ld(dst_t, 0), _ld(dst_t, 1), _ptr(scale_t),
+                            _ld(scale_t, 0), _ld(scale_t, 1), G, rows, cols, block_rows, dt)
+    _check(_lib.rm_quantize_fp8_block(ctypes.byref(a), _stream(stream)), what)
+
+
+def rm_matmul_fp8_block(A, A_scale, W, W_scale, out, out_scale=None, bias=None, act=None, resid=None,
+                        w_block_rows: int = 128, device_status=None, wait_budget_ns: int = 0, stream=None) -> None:
+    """out = act(A W^T + bias) + resid for A [M, K] or [G, M, K] and W [N, K] or [G, N, K] in e4m3 with scales for
+    each 1 x 128 block of A and w_block_rows x 128 block of W (a group dimension of stride 0 is shared).  out is
+    bfloat16, float32 (resid has its type and may be out) or e4m3 with out_scale.  act: None, "tanh", "erf",
+    "relu"."""
+    what = "rm_matmul_fp8_block"
+    if A.dim() == 2:
+        A, A_scale, W, W_scale, out, out_scale, resid = (
+            t if t is None else t.unsqueeze(0) for t in (A, A_scale, W, W_scale, out, out_scale, resid))
+        bias = bias if bias is None else bias.unsqueeze(0)
+    if A.dim() != 3 or W.dim() != 3:
+        _refuse(what, "A and W are not both [rows, K] or both [G, rows, K]")
+    G, M, K = A.shape
+    N = W.shape[1]
+    if w_block_rows not in (1, 128):
+        _refuse(what, "w_block_rows is neither 1 nor 128")
+    if act not in _FP8_ACTS:
+        _refuse(what, f"unknown activation {act!r}")
+    _need(what, _current_device(), A=A, A_scale=A_scale, W=W, W_scale=W_scale, out=out, out_scale=out_scale, bias=bias,
+          resid=resid, device_status=device_status)
+    _bytes8(what, A=A, A_scale=A_scale, W=W, W_scale=W_scale, out_scale=out_scale)
+    _f32(what, bias=bias)
+    odt = _stream_dtypes().get(out.dtype, RM_E4M3 if out.element_size() == 1 else None)
+    if odt is None:
+        _refuse(what, "out is neither bfloat16, float32 nor 8-bit")
+    nb = (K + 127) // 128
+    _shape(what, "A_scale", A_scale, (G, M, nb))
+    _shape(what, "W", W, (G, N, K))
+    _shape(what, "W_scale", W_scale, (G, -(-N // w_block_rows), nb))
+    _shape(what, "out", out, (G, M, N))
+    _shape(what, "out_scale", out_scale, (G, M, (N + 127) // 128))
+    _shape(what, "bias", bias, (G, N))
+    _shape(what, "resid", resid, (G, M, N))
+    if bias is not None and not bias.is_contiguous():
+        _refuse(what, "bias is not contiguous")
+    if resid is not None and resid.dtype != out.dtype:
+        _refuse(what, "resid has another type than out")
+    if device_status is not None and device_status.dtype.itemsize != 4:
+        _refuse(what, "device_status is not a 32-bit integer")
+    a = rm_matmul_fp8_args(
+        _ptr(A), _ld(A, 0), _ld(A, 1), _ptr(A_scale), _ld(A_scale, 0), _ld(A_scale, 1), _ptr(W), _ld(W, 0), _ld(W, 1),
+        _ptr(W_scale), _ld(W_scale, 0), _ld(W_scale, 1), _ptr(bias), _ptr(resid), _ld(resid, 0), _ld(resid, 1),
+        _ptr(out), _ld(out, 0), _ld(out, 1), _ptr(out_scale), _ld(out_scale, 0), _ld(out_scale, 1), _ptr(device_status),
+        wait_budget_ns, G, M, N, K, w_block_rows, _FP8_ACTS[act], odt)
+    _check(_lib.rm_matmul_fp8_block(ctypes.byref(a), _stream(stream)), what)
