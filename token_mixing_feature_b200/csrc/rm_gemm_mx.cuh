@@ -1,0 +1,145 @@
+// Shared by the two kernels of the block-scaled 8-bit product: arguments,
+// activations, waits and launch helpers.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "rm_mx.cuh"
+#include "rm_tmap.h"
+
+namespace rm {
+
+struct MxParams {
+    int G, M, N, K;
+    int a_g_inner, w_g_inner;   // map coordinate order (k, g, row) if 1, else (k, row, g)
+    int a_gmul, w_gmul;         // 0: the operand is shared by all groups
+    const uint8_t* a_scale;
+    long long as_gs, as_ld;
+    const uint8_t* w_scale;
+    long long ws_gs, ws_ld;
+    int w_shift;                // row n's scales are row n >> w_shift of w_scale
+    int a_vec, w_vec;           // the scale rows start on 4-byte boundaries
+    const float* bias;
+    const void* resid;
+    long long r_gs, r_ld;
+    int o_g_inner;              // map coordinate order of out (pair kernel)
+    long long o_gs, o_ld;       // (few-row kernel)
+    uint8_t* out_scale;
+    long long os_gs, os_ld;
+    int act;
+    DeviceErr err;
+    unsigned long long budget_ns;
+};
+
+__device__ __forceinline__ float exp2_approx(float x) {   // within 2^-22 of the value
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float2 exp2_pair(float2 x) { return make_float2(exp2_approx(x.x), exp2_approx(x.y)); }
+__device__ __forceinline__ float2 rcp_pair(float2 x) {
+    float2 y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(x.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(x.y));
+    return y;
+}
+
+// act(v) of a pair, without branches.  GELU's tanh form goes through
+// tanh.approx (absolute error 2^-10.9 of tanh) where the result is stored in 16
+// or 8 bits; for fp32 results it is v * sigmoid(2u), u = sqrt(2/pi) (v +
+// 0.044715 v^3).  The erf form takes Abramowitz and Stegun's 7.1.26,
+// erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2), t = 1 / (1 + 0.3275911 x), x >= 0,
+// whose error is at most 1.5e-7, on the side where nothing cancels.
+template <int ACT, bool PRECISE>
+__device__ __forceinline__ float2 activation(float2 v) {
+    if constexpr (ACT == RM_ACT_GELU_TANH && !PRECISE) {
+        return gelu_tanh_pair(v);
+    } else if constexpr (ACT == RM_ACT_GELU_TANH) {
+        const float c = -2.0f * 0.7978845608028654f * 1.4426950408889634f;   // -2 sqrt(2/pi) log2(e)
+        const float2 e = exp2_pair(f2_mul(v, f2_fma(f2_mul(v, v), f2(c * 0.044715f), f2(c))));
+        return f2_mul(v, rcp_pair(f2_add(e, f2(1.0f))));
+    } else if constexpr (ACT == RM_ACT_GELU_ERF) {
+        const float2 x = f2_mul(make_float2(fabsf(v.x), fabsf(v.y)), f2(0.7071067811865476f));
+        const float2 t = rcp_pair(f2_fma(x, f2(0.3275911f), f2(1.0f)));
+        float2 q = f2_fma(t, f2(1.061405429f), f2(-1.453152027f));
+        q = f2_fma(t, q, f2(1.421413741f));
+        q = f2_fma(t, q, f2(-0.284496736f));
+        q = f2_fma(t, q, f2(0.254829592f));
+        const float2 e = exp2_pair(f2_mul(f2_mul(v, v), f2(-0.5f * 1.4426950408889634f)));   // exp(-x^2)
+        const float2 hc = f2_mul(f2_mul(f2_mul(q, t), e), f2(0.5f));   // erfc(x) / 2
+        return f2_mul(v, make_float2(v.x < 0.f ? hc.x : 1.0f - hc.x, v.y < 0.f ? hc.y : 1.0f - hc.y));
+    } else {
+        return make_float2(v.x < 0.f ? 0.f : v.x, v.y < 0.f ? 0.f : v.y);   // (keeps NaN)
+    }
+}
+template <int ACT, bool PRECISE, int NV>
+__device__ __forceinline__ void activate(float (&v)[NV]) {
+#pragma unroll
+    for (int e = 0; e < NV; e += 2) {
+        const float2 y = activation<ACT, PRECISE>(make_float2(v[e], v[e + 1]));
+        v[e] = y.x, v[e + 1] = y.y;
+    }
+}
+
+// A wait of a whole warp: all lanes go on, or none.  CLUSTER: for what the
+// pair's other CTA released.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtx& w, int site) {
+    return __all_sync(0xffffffffu, CLUSTER ? mbar_wait_cluster(bar, parity, w, site) : mbar_wait(bar, parity, w, site));
+}
+
+// Map of [G][rows][cols] elements of esz bytes with a box of `box` rows x 128
+// bytes: dims (cols, rows, groups) with the smaller of the two strides first.
+// A single row or group takes any legal stride; a group stride of 0 is an
+// input that all groups share.
+inline bool matrix_map(CUtensorMap* m, const void* base, int cols, int rows, int G, long long ld, long long gs, int esz,
+                uint32_t box, int* g_inner, int* gmul) {
+    if (gmul) *gmul = gs == 0 ? 0 : 1;
+    if (gs == 0) G = 1;
+    if (rows == 1) ld = ((long long)cols + 15) / 16 * 16;
+    if (G == 1) gs = rows * ld;
+    *g_inner = gs < ld ? 1 : 0;
+    return *g_inner ? make_map_e(m, base, cols, G, rows, gs * esz, ld * esz, 1, box, esz)
+                    : make_map_e(m, base, cols, rows, G, ld * esz, gs * esz, box, 1, esz);
+}
+
+// The opt-in to more than 48 KB of shared memory, once per kernel and device.
+struct SmemGrant {
+    bool done[64] = {};
+    template <typename F>
+    cudaError_t ask(F* kernel, int bytes) {
+        int d = 0;
+        cudaError_t e = cudaGetDevice(&d);
+        if (e != cudaSuccess || (d < 64 && __atomic_load_n(&done[d], __ATOMIC_ACQUIRE))) return e;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess && d < 64) __atomic_store_n(&done[d], true, __ATOMIC_RELEASE);
+        return e;
+    }
+};
+
+
+// Programmatic launch with clusters of `cluster` CTAs.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s,
+                           Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// Few rows (rm_gemm_mx_few.cu).
+cudaError_t launch_gemm_mx_few(const rm_matmul_fp8_args& a, MxParams& p, int num_sms, cudaStream_t s);
+
+}  // namespace rm

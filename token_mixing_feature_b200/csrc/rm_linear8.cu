@@ -49,9 +49,9 @@ rm_status rm_rmsnorm_forward(const rm_rmsnorm_args* a, rm_stream_t stream) {
         return RM_ERR_INVALID_ARG;
     if (a->D % 16 || a->D > 16384 || a->rows > 0x7fffffffLL) return RM_ERR_UNSUPPORTED;
     const int esz = a->dtype == RM_BF16 ? 2 : 4;
+    if (a->rows == 0) return RM_OK;   // (before the pointers: an empty array's may be null)
     if ((a->Yq == nullptr) != (a->Ys == nullptr)) return RM_ERR_INVALID_ARG;
     if (!a->Sum && !a->Y && !a->Yq && !a->rstd) return RM_ERR_INVALID_ARG;
-    if (a->rows == 0) return RM_OK;
     if (!al16(a->X) || !row_stride(a->ld_x, a->rows, a->D, esz) || !al16_or_null(a->gamma) || !al(a->rstd, 4))
         return RM_ERR_INVALID_ARG;
     if (a->R && (!al16(a->R) || !row_stride(a->ld_r, a->rows, a->D, esz))) return RM_ERR_INVALID_ARG;
@@ -98,11 +98,11 @@ rm_status rm_quantize_fp8_block(const rm_quant_block_args* a, rm_stream_t stream
     if (!a || (a->dtype != RM_BF16 && a->dtype != RM_F32) || a->G < 0 || a->rows < 0 || a->cols < 1)
         return RM_ERR_INVALID_ARG;
     if (a->block_rows != 1 && a->block_rows != 128) return RM_ERR_INVALID_ARG;
-    if ((!a->dst && !a->dst_t) || (a->dst && !a->scale) || (a->dst_t && !a->scale_t)) return RM_ERR_INVALID_ARG;
     if (a->cols % 16) return RM_ERR_UNSUPPORTED;
     if (a->rows > 0x7fffff00 || (double)a->G * blocks(a->rows) * blocks(a->cols) > 2147483647.0)
         return RM_ERR_UNSUPPORTED;
     if (a->G == 0 || a->rows == 0) return RM_OK;
+    if ((!a->dst && !a->dst_t) || (a->dst && !a->scale) || (a->dst_t && !a->scale_t)) return RM_ERR_INVALID_ARG;
     const int esz = a->dtype == RM_BF16 ? 2 : 4, br = a->block_rows;
     if (!al16(a->src) || !row_stride(a->src_ld, a->rows, a->cols, esz) ||
         !group_stride(a->src_gstride, a->G, esz, true))
