@@ -448,85 +448,102 @@ def rm_stack_forward_fp8(h: Handle, blocks: Sequence[Dict], qblocks: Sequence[Di
 # These take torch tensors (strided views are fine as long as the last dimension
 # is contiguous), read sizes and strides off them and refuse what the C call
 # cannot see: wrong types, shapes or devices.  8-bit tensors are uint8 or
-# float8_e4m3fn, scale bytes uint8 or float8_e8m0fnu.
-_FP8_ACTS = {**ACTS, "none": RM_ACT_NONE, None: RM_ACT_NONE}
+# float8_e4m3fn, scale bytes uint8 or float8_e8m0fnu.  Their calls are as short
+# as the kernels of a serving step, so the checks are kept to one pass over each
+# tensor's metadata.
+class _Torch:
+    """torch's names that these wrappers use, looked up once (on the first call)."""
+
+    def __init__(self):
+        import torch
+        torch.cuda.init()
+        self.device, self.stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        self.f32, self.streams = torch.float32, {torch.bfloat16: RM_BF16, torch.float32: RM_F32}
+        self.codes = frozenset((torch.uint8, torch.float8_e4m3fn))
+        self.scales = frozenset((torch.uint8, torch.float8_e8m0fnu))
+        self.outs = {**self.streams, **{c: RM_E4M3 for c in self.codes}}
+        self.i32 = frozenset((torch.int32,))
+
+
+_torch: Optional[_Torch] = None
+
+
+def _rt() -> _Torch:
+    global _torch
+    if _torch is None:
+        _torch = _Torch()
+    return _torch
 
 
 def _refuse(what: str, why: str):
     raise RankMixerError(RM_ERR_INVALID_ARG, f"{what}: {why}")
 
 
-def _stream_dtypes():
-    import torch
-    return {torch.bfloat16: RM_BF16, torch.float32: RM_F32}
-
-
-def _need(what: str, device: int, **tensors) -> None:
-    """Every tensor that is given lies on the current device `device`, its last dimension contiguous."""
-    for name, t in tensors.items():
-        if t is not None:
-            if t.get_device() != device:
-                _refuse(what, f"{name} is not on the current CUDA device")
-            if t.stride(-1) != 1 and t.shape[-1] > 1:
-                _refuse(what, f"{name}'s last dimension is not contiguous")
-
-
-def _shape(what: str, name: str, t, shape) -> None:
-    if t is not None and tuple(t.shape) != tuple(shape):
-        _refuse(what, f"{name} has shape {tuple(t.shape)}, wanted {tuple(shape)}")
-
-
-def _bytes8(what: str, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.element_size() != 1:
-            _refuse(what, f"{name} holds no 8-bit values")
-
-
-def _f32(what: str, **tensors) -> None:
-    import torch
-    for name, t in tensors.items():
-        if t is not None and t.dtype != torch.float32:
-            _refuse(what, f"{name} is not float32")
-
-
-def _ld(t, dim: int = 0) -> int:
-    """Stride of a dimension (0 if there is no tensor); the last dimension's extent, rounded up to what every
-    type's 16-byte rows take, where the dimension has one entry and torch's stride means nothing."""
+def _wrong(what: str, name: str, t, dtypes, shape, device):
     if t is None:
-        return 0
-    return t.stride(dim) if t.shape[dim] > 1 else (t.shape[-1] + 15) // 16 * 16
+        _refuse(what, f"{name} is missing")
+    _refuse(what, f"{name} is {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}; wanted "
+                  f"{' or '.join(str(d) for d in dtypes)} {tuple(shape)}, contiguous in the last dimension, on the current "
+                  f"CUDA device (cuda:{device})")
 
 
-def _current_device() -> int:
-    import torch
-    return torch.cuda.current_device()
+def _vec(what: str, name: str, t, dtype, n: int, device: int):
+    """Address of a contiguous vector [n] (None for None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != (n,) or t.get_device() != device or (n > 1 and t.stride(0) != 1):
+        _wrong(what, name, t, (dtype,), (n,), device)
+    return t.data_ptr()
+
+
+def _mat(what: str, name: str, t, dtypes, shape, device: int):
+    """Address and row stride of a matrix of that shape (None and 0 for None).  A single row's stride means nothing
+    to torch or to the library."""
+    if t is None:
+        return None, 0
+    rows, ld = t.shape, t.stride()
+    if t.dtype not in dtypes or rows != shape or t.get_device() != device or (ld[1] != 1 and rows[1] > 1):
+        _wrong(what, name, t, dtypes, shape, device)
+    return t.data_ptr(), ld[0]
+
+
+def _grp(what: str, name: str, t, dtypes, shape, device: int):
+    """Address, group stride and row stride of [G, rows, cols] (None and zeros for None)."""
+    if t is None:
+        return None, 0, 0
+    s = t.stride()
+    if t.dtype not in dtypes or t.shape != shape or t.get_device() != device or (s[2] != 1 and shape[2] > 1):
+        _wrong(what, name, t, dtypes, shape, device)
+    return t.data_ptr(), s[0], s[1]
+
+
+def _row_stream(what: str, name: str, t, rt: _Torch):
+    """(rm_dtype, {torch dtype}) of a bf16 or fp32 activation tensor."""
+    dt = rt.streams.get(t.dtype)
+    if dt is None:
+        _refuse(what, f"{name} is neither bfloat16 nor float32")
+    return dt, (t.dtype,)
 
 
 def rm_rmsnorm_forward(X, R=None, gamma=None, Sum=None, Y=None, Yq=None, Ys=None, rstd=None, eps: float = 1e-5,
                        stream=None) -> None:
     """s = X + R, y = s / sqrt(mean(s^2) + eps) * gamma for rows X [rows, D]; outputs Sum (s), Y (y), Yq and Ys
     (y in e4m3 with a scale for each 128), rstd, each of them optional."""
-    what = "rm_rmsnorm_forward"
-    if X.dim() != 2:
+    what, rt = "rm_rmsnorm_forward", _rt()
+    dev, shape = rt.device(), X.shape
+    if len(shape) != 2:
         _refuse(what, "X is not [rows, D]")
-    dt = _stream_dtypes().get(X.dtype)
-    if dt is None:
-        _refuse(what, "X is neither bfloat16 nor float32")
-    rows, D = X.shape
-    _need(what, _current_device(), X=X, R=R, gamma=gamma, Sum=Sum, Y=Y, Yq=Yq, Ys=Ys, rstd=rstd)
-    for name, t in (("R", R), ("Sum", Sum), ("Y", Y)):
-        if t is not None and t.dtype != X.dtype:
-            _refuse(what, f"{name} has another type than X")
-        _shape(what, name, t, (rows, D))
-    _f32(what, gamma=gamma, rstd=rstd)
-    _bytes8(what, Yq=Yq, Ys=Ys)
-    _shape(what, "gamma", gamma, (D,))
-    _shape(what, "rstd", rstd, (rows,))
-    _shape(what, "Yq", Yq, (rows, D))
-    _shape(what, "Ys", Ys, (rows, (D + 127) // 128))
-    a = rm_rmsnorm_args(_ptr(X), _ptr(R), _ptr(gamma), _ptr(Sum), _ptr(Y), _ptr(Yq), _ptr(Ys), _ptr(rstd), _ld(X),
-                        _ld(R), _ld(Sum), _ld(Y), _ld(Yq), _ld(Ys), rows, D, dt, eps)
-    _check(_lib.rm_rmsnorm_forward(ctypes.byref(a), _stream(stream)), what)
+    dt, same = _row_stream(what, "X", X, rt)
+    rows, D = shape
+    x, ldx = _mat(what, "X", X, same, shape, dev)
+    r, ldr = _mat(what, "R", R, same, shape, dev)
+    sm, lds = _mat(what, "Sum", Sum, same, shape, dev)
+    y, ldy = _mat(what, "Y", Y, same, shape, dev)
+    q, ldq = _mat(what, "Yq", Yq, rt.codes, shape, dev)
+    qs, ldqs = _mat(what, "Ys", Ys, rt.scales, (rows, (D + 127) // 128), dev)
+    a = rm_rmsnorm_args(x, r, _vec(what, "gamma", gamma, rt.f32, D, dev), sm, y, q, qs,
+                        _vec(what, "rstd", rstd, rt.f32, rows, dev), ldx, ldr, lds, ldy, ldq, ldqs, rows, D, dt, eps)
+    _check(_lib.rm_rmsnorm_forward(a, rt.stream(dev) if stream is None else _stream(stream)), what)
 
 
 def rm_rmsnorm_backward_workspace_bytes(rows: int, D: int) -> int:
@@ -537,29 +554,25 @@ def rm_rmsnorm_backward(dY, S, gamma, rstd, dSum, dX, dgamma=None, workspace=Non
     """dX = dL/dX (= dL/dR) and dgamma of rm_rmsnorm_forward from dY = dL/dy, the saved S and rstd, and dSum, the
     gradient that reaches Sum from elsewhere (or None).  dgamma needs a workspace of
     rm_rmsnorm_backward_workspace_bytes(rows, D) bytes."""
-    what = "rm_rmsnorm_backward"
-    if S.dim() != 2:
+    what, rt = "rm_rmsnorm_backward", _rt()
+    dev, shape = rt.device(), S.shape
+    if len(shape) != 2:
         _refuse(what, "S is not [rows, D]")
-    dt = _stream_dtypes().get(S.dtype)
-    if dt is None:
-        _refuse(what, "S is neither bfloat16 nor float32")
-    rows, D = S.shape
-    _need(what, _current_device(), dY=dY, S=S, gamma=gamma, rstd=rstd, dSum=dSum, dX=dX, dgamma=dgamma,
-          workspace=workspace)
-    for name, t in (("dY", dY), ("dSum", dSum), ("dX", dX)):
-        if t is not None and t.dtype != S.dtype:
-            _refuse(what, f"{name} has another type than S")
-        _shape(what, name, t, (rows, D))
-    _f32(what, gamma=gamma, rstd=rstd, dgamma=dgamma)
-    _shape(what, "gamma", gamma, (D,))
-    _shape(what, "rstd", rstd, (rows,))
-    _shape(what, "dgamma", dgamma, (D,))
-    if workspace is not None and not workspace.is_contiguous():
-        _refuse(what, "the workspace is not contiguous")
-    a = rm_rmsnorm_grad_args(_ptr(dY), _ptr(S), _ptr(dSum), _ptr(gamma), _ptr(rstd), _ptr(dX), _ptr(dgamma),
-                             _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
-                             _ld(dY), _ld(S), _ld(dSum), _ld(dX), rows, D, dt)
-    _check(_lib.rm_rmsnorm_backward(ctypes.byref(a), _stream(stream)), what)
+    dt, same = _row_stream(what, "S", S, rt)
+    rows, D = shape
+    s, lds = _mat(what, "S", S, same, shape, dev)
+    dy, lddy = _mat(what, "dY", dY, same, shape, dev)
+    ds, ldds = _mat(what, "dSum", dSum, same, shape, dev)
+    dx, lddx = _mat(what, "dX", dX, same, shape, dev)
+    ws = nbytes = 0
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            _refuse(what, "the workspace is not contiguous memory of the current CUDA device")
+        ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    a = rm_rmsnorm_grad_args(dy, s, ds, _vec(what, "gamma", gamma, rt.f32, D, dev),
+                             _vec(what, "rstd", rstd, rt.f32, rows, dev), dx, _vec(what, "dgamma", dgamma, rt.f32, D, dev),
+                             ws, nbytes, lddy, lds, ldds, lddx, rows, D, dt)
+    _check(_lib.rm_rmsnorm_backward(a, rt.stream(dev) if stream is None else _stream(stream)), what)
 
 
 def rm_quantize_fp8_block(src, dst=None, scale=None, dst_t=None, scale_t=None, block_rows: int = 1,
@@ -567,72 +580,67 @@ def rm_quantize_fp8_block(src, dst=None, scale=None, dst_t=None, scale_t=None, b
     """src [rows, cols] or [G, rows, cols] to e4m3 dst (same shape) with scale [.., ceil(rows / block_rows),
     ceil(cols / 128)], and / or to its transpose dst_t [.., cols, rows] with scale_t [.., ceil(cols / block_rows),
     ceil(rows / 128)]."""
-    what = "rm_quantize_fp8_block"
+    what, rt = "rm_quantize_fp8_block", _rt()
+    dev = rt.device()
     if src.dim() == 2:
         src, dst, scale, dst_t, scale_t = (t if t is None else t.unsqueeze(0) for t in (src, dst, scale, dst_t, scale_t))
-    if src.dim() != 3:
+    shape = src.shape
+    if len(shape) != 3:
         _refuse(what, "src is neither [rows, cols] nor [G, rows, cols]")
-    dt = _stream_dtypes().get(src.dtype)
-    if dt is None:
-        _refuse(what, "src is neither bfloat16 nor float32")
-    if block_rows not in (1, 128):
+    dt, same = _row_stream(what, "src", src, rt)
+    if block_rows != 1 and block_rows != 128:
         _refuse(what, "block_rows is neither 1 nor 128")
-    G, rows, cols = src.shape
-    _need(what, _current_device(), src=src, dst=dst, scale=scale, dst_t=dst_t, scale_t=scale_t)
-    _bytes8(what, dst=dst, scale=scale, dst_t=dst_t, scale_t=scale_t)
-    _shape(what, "dst", dst, (G, rows, cols))
-    _shape(what, "scale", scale, (G, -(-rows // block_rows), (cols + 127) // 128))
-    _shape(what, "dst_t", dst_t, (G, cols, rows))
-    _shape(what, "scale_t", scale_t, (G, -(-cols // block_rows), (rows + 127) // 128))
-    a = rm_quant_block_args(_ptr(src), _ld(src, 0), _ld(src, 1), _ptr(dst), _ld(dst, 0), _ld(dst, 1), _ptr(scale),
-                            _ld(scale, 0), _ld(scale, 1), _ptr(dst_t), _ld(dst_t, 0), _ld(dst_t, 1), _ptr(scale_t),
-                            _ld(scale_t, 0), _ld(scale_t, 1), G, rows, cols, block_rows, dt)
-    _check(_lib.rm_quantize_fp8_block(ctypes.byref(a), _stream(stream)), what)
+    G, rows, cols = shape
+    a = rm_quant_block_args(
+        *_grp(what, "src", src, same, shape, dev), *_grp(what, "dst", dst, rt.codes, shape, dev),
+        *_grp(what, "scale", scale, rt.scales, (G, -(-rows // block_rows), (cols + 127) // 128), dev),
+        *_grp(what, "dst_t", dst_t, rt.codes, (G, cols, rows), dev),
+        *_grp(what, "scale_t", scale_t, rt.scales, (G, -(-cols // block_rows), (rows + 127) // 128), dev),
+        G, rows, cols, block_rows, dt)
+    _check(_lib.rm_quantize_fp8_block(a, rt.stream(dev) if stream is None else _stream(stream)), what)
+
+
+_FP8_ACTS = {**ACTS, "none": RM_ACT_NONE, None: RM_ACT_NONE}
 
 
 def rm_matmul_fp8_block(A, A_scale, W, W_scale, out, out_scale=None, bias=None, act=None, resid=None,
                         w_block_rows: int = 128, device_status=None, wait_budget_ns: int = 0, stream=None) -> None:
     """out = act(A W^T + bias) + resid for A [M, K] or [G, M, K] and W [N, K] or [G, N, K] in e4m3 with scales for
     each 1 x 128 block of A and w_block_rows x 128 block of W (a group dimension of stride 0 is shared).  out is
-    bfloat16, float32 (resid has its type and may be out) or e4m3 with out_scale.  act: None, "tanh", "erf",
-    "relu"."""
-    what = "rm_matmul_fp8_block"
+    bfloat16, float32 (resid has its type and may be out) or e4m3 with out_scale; bias float32 [N] or [G, N].
+    act: None, "tanh", "erf", "relu"."""
+    what, rt = "rm_matmul_fp8_block", _rt()
+    dev = rt.device()
     if A.dim() == 2:
-        A, A_scale, W, W_scale, out, out_scale, resid = (
-            t if t is None else t.unsqueeze(0) for t in (A, A_scale, W, W_scale, out, out_scale, resid))
-        bias = bias if bias is None else bias.unsqueeze(0)
-    if A.dim() != 3 or W.dim() != 3:
+        A, A_scale, W, W_scale, out, out_scale, bias, resid = (
+            t if t is None else t.unsqueeze(0) for t in (A, A_scale, W, W_scale, out, out_scale, bias, resid))
+    shape = A.shape
+    if len(shape) != 3 or W.dim() != 3:
         _refuse(what, "A and W are not both [rows, K] or both [G, rows, K]")
-    G, M, K = A.shape
+    G, M, K = shape
     N = W.shape[1]
-    if w_block_rows not in (1, 128):
+    if w_block_rows != 1 and w_block_rows != 128:
         _refuse(what, "w_block_rows is neither 1 nor 128")
-    if act not in _FP8_ACTS:
+    code = _FP8_ACTS.get(act)
+    if code is None:
         _refuse(what, f"unknown activation {act!r}")
-    _need(what, _current_device(), A=A, A_scale=A_scale, W=W, W_scale=W_scale, out=out, out_scale=out_scale, bias=bias,
-          resid=resid, device_status=device_status)
-    _bytes8(what, A=A, A_scale=A_scale, W=W, W_scale=W_scale, out_scale=out_scale)
-    _f32(what, bias=bias)
-    odt = _stream_dtypes().get(out.dtype, RM_E4M3 if out.element_size() == 1 else None)
+    odt = rt.outs.get(out.dtype)
     if odt is None:
-        _refuse(what, "out is neither bfloat16, float32 nor 8-bit")
-    nb = (K + 127) // 128
-    _shape(what, "A_scale", A_scale, (G, M, nb))
-    _shape(what, "W", W, (G, N, K))
-    _shape(what, "W_scale", W_scale, (G, -(-N // w_block_rows), nb))
-    _shape(what, "out", out, (G, M, N))
-    _shape(what, "out_scale", out_scale, (G, M, (N + 127) // 128))
-    _shape(what, "bias", bias, (G, N))
-    _shape(what, "resid", resid, (G, M, N))
-    if bias is not None and not bias.is_contiguous():
-        _refuse(what, "bias is not contiguous")
-    if resid is not None and resid.dtype != out.dtype:
-        _refuse(what, "resid has another type than out")
-    if device_status is not None and device_status.dtype.itemsize != 4:
-        _refuse(what, "device_status is not a 32-bit integer")
+        _refuse(what, "out is neither bfloat16, float32 nor e4m3")
+    nb, oshape, same = (K + 127) // 128, (G, M, N), (out.dtype,)
+    b = status = None
+    if bias is not None:
+        b = _grp(what, "bias", bias.unsqueeze(1), (rt.f32,), (G, 1, N), dev)
+        if b[1] != N and G > 1:
+            _wrong(what, "bias", bias, (rt.f32,), (G, N), dev)
+        b = b[0]
+    if device_status is not None:
+        status = _mat(what, "device_status", device_status.view(1, 1), rt.i32, (1, 1), dev)[0]
     a = rm_matmul_fp8_args(
-        _ptr(A), _ld(A, 0), _ld(A, 1), _ptr(A_scale), _ld(A_scale, 0), _ld(A_scale, 1), _ptr(W), _ld(W, 0), _ld(W, 1),
-        _ptr(W_scale), _ld(W_scale, 0), _ld(W_scale, 1), _ptr(bias), _ptr(resid), _ld(resid, 0), _ld(resid, 1),
-        _ptr(out), _ld(out, 0), _ld(out, 1), _ptr(out_scale), _ld(out_scale, 0), _ld(out_scale, 1), _ptr(device_status),
-        wait_budget_ns, G, M, N, K, w_block_rows, _FP8_ACTS[act], odt)
-    _check(_lib.rm_matmul_fp8_block(ctypes.byref(a), _stream(stream)), what)
+        *_grp(what, "A", A, rt.codes, shape, dev), *_grp(what, "A_scale", A_scale, rt.scales, (G, M, nb), dev),
+        *_grp(what, "W", W, rt.codes, (G, N, K), dev),
+        *_grp(what, "W_scale", W_scale, rt.scales, (G, -(-N // w_block_rows), nb), dev), b,
+        *_grp(what, "resid", resid, same, oshape, dev), *_grp(what, "out", out, same, oshape, dev),
+        *_grp(what, "out_scale", out_scale, rt.scales, (G, M, (N + 127) // 128), dev), status, wait_budget_ns,
+        G, M, N, K, w_block_rows, code, odt)
+    _check(_lib.rm_matmul_fp8_block(a, rt.stream(dev) if stream is None else _stream(stream)), what)
