@@ -133,29 +133,29 @@ __device__ __forceinline__ void finish(float (&v)[kFrag], const MxParams& p, uin
 }
 
 // e4m3 output: the scale of each of the thread's two rows (its quad's largest
-// magnitude over the columns below N), the byte to memory; inv: 2^-e as float
-// bits, or NaN for a NaN block (whose codes come out as NaN by themselves).
-__device__ __forceinline__ void row_scales(const float (&v)[kFrag], uint32_t (&inv)[2], const MxParams& p, int g, int row0,
+// magnitude over the columns below N), the byte to memory; inv: its inverse.
+__device__ __forceinline__ void row_scales(const float (&v)[kFrag], float (&inv)[2], const MxParams& p, int g, int row0,
                                            int n, int lane) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        uint32_t mx = 0;
+        float mf = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            if (n + 8 * i < p.N) mx = max(mx, max(abs_bits(v[4 * i + 2 * h]), abs_bits(v[4 * i + 2 * h + 1])));
+            if (n + 8 * i < p.N) mf = max_abs(mf, make_float2(v[4 * i + 2 * h], v[4 * i + 2 * h + 1]));
+        uint32_t mx = abs_bits(mf);
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         const uint32_t b = scale_byte(mx);
         const int m = row0 + (lane >> 2) + 8 * h;
         if ((lane & 3) == 0 && m < p.M) p.out_scale[g * p.os_gs + m * p.os_ld + (n >> 7)] = (uint8_t)b;
-        inv[h] = b == 255u ? 0x7fffffffu : (254u - b) << 23;
+        inv[h] = scale_inverse(b);
     }
 }
 
 // One box (16 rows x 128 bytes, in the 128-byte swizzle of the bulk stores) of
 // the half: all 128 columns of e4m3, 64 of bf16, 32 of fp32.
 template <int OUT>
-__device__ __forceinline__ void stage_box(const float* v, uint32_t buf, const uint32_t (&inv)[2], int lane) {
+__device__ __forceinline__ void stage_box(const float* v, uint32_t buf, const float (&inv)[2], int lane) {
     const int q = lane & 3, r7 = lane >> 2;   // row lane / 4 + 8 h: the swizzle's row is r7 for both h
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -170,7 +170,7 @@ __device__ __forceinline__ void stage_box(const float* v, uint32_t buf, const ui
                 sts64(row + (((2 * i + q / 2) ^ r7) << 4) + 8 * (q & 1),
                       make_uint2(__float_as_uint(v[4 * i + 2 * h]), __float_as_uint(v[4 * i + 2 * h + 1])));
         } else {
-            const float2 k = f2(__uint_as_float(inv[h]));
+            const float2 k = f2(inv[h]);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const float2 y = f2_mul(make_float2(v[4 * i + 2 * h], v[4 * i + 2 * h + 1]), k);
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int r0 = row0 + 16 * h;
                 if (r0 >= p.M || n >= p.N) continue;   // (one value per warp)
                 finish<OUT>(v, p, bias_s, t.g, r0, n, lane);
-                uint32_t inv[2] = {0u, 0u};
+                float inv[2] = {0.f, 0.f};
                 if constexpr (OUT == RM_E4M3) row_scales(v, inv, p, t.g, r0, n, lane);
 #pragma unroll
                 for (int b = 0; b < BOXES; ++b) {

@@ -104,21 +104,6 @@ inline bool matrix_map(CUtensorMap* m, const void* base, int cols, int rows, int
                     : make_map_e(m, base, cols, rows, G, ld * esz, gs * esz, box, 1, esz);
 }
 
-// The opt-in to more than 48 KB of shared memory, once per kernel and device.
-struct SmemGrant {
-    bool done[64] = {};
-    template <typename F>
-    cudaError_t ask(F* kernel, int bytes) {
-        int d = 0;
-        cudaError_t e = cudaGetDevice(&d);
-        if (e != cudaSuccess || (d < 64 && __atomic_load_n(&done[d], __ATOMIC_ACQUIRE))) return e;
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e == cudaSuccess && d < 64) __atomic_store_n(&done[d], true, __ATOMIC_RELEASE);
-        return e;
-    }
-};
-
-
 // Programmatic launch with clusters of `cluster` CTAs.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s,

@@ -65,11 +65,11 @@ __device__ __forceinline__ void put_row(float4 x, const MxParams& p, void* out, 
         if (in) mx = max(max(abs_bits(v[0]), abs_bits(v[1])), max(abs_bits(v[2]), abs_bits(v[3])));
         mx = __reduce_max_sync(0xffffffffu, mx);
         const uint32_t b = scale_byte(mx);
-        const float inv = scale_inverse(min(b, 254u));
+        const float2 inv = f2(scale_inverse(b));
         if (lane == 0 && in) p.out_scale[g * p.os_gs + m * p.os_ld + (n >> 7)] = (uint8_t)b;
         if (in)
             *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(out) + g * p.o_gs + m * p.o_ld + n) =
-                b == 255u ? kNanCodes : e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+                e4m3x4(f2_mul(make_float2(v[0], v[1]), inv), f2_mul(make_float2(v[2], v[3]), inv));
     } else if (in) {
         const long long r = g * p.r_gs + m * p.r_ld + n, o = g * p.o_gs + m * p.o_ld + n;
         if constexpr (OUT == RM_F32) {

@@ -243,12 +243,12 @@ struct RmsNormGrad {
     const void *dY, *S, *dSum;
     const float *gamma, *rstd;
     void* dX;
-    float* part;   // [rmsnorm_bwd_parts][D], or null: no dgamma
+    float* part;   // [rmsnorm_bwd_parts(rows)][D], or null: no dgamma
     long long ld_dy, ld_s, ld_dsum, ld_dx;
     long long rows;
     int D;
 };
-int rmsnorm_bwd_parts(long long rows, int D);
+int rmsnorm_bwd_parts(long long rows);
 cudaError_t launch_rmsnorm_bwd(int dtype, const RmsNormGrad& p, float* dgamma, cudaStream_t s);
 struct QuantBlock {
     const void* src;

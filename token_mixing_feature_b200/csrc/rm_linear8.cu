@@ -69,7 +69,7 @@ rm_status rm_rmsnorm_forward(const rm_rmsnorm_args* a, rm_stream_t stream) {
 
 size_t rm_rmsnorm_backward_workspace_bytes(long long rows, int D) {
     if (rows < 1 || D < 1 || D % 16 || D > 16384) return 0;
-    return sizeof(float) * (size_t)rm::rmsnorm_bwd_parts(rows, D) * D;
+    return sizeof(float) * (size_t)rm::rmsnorm_bwd_parts(rows) * D;
 }
 
 rm_status rm_rmsnorm_backward(const rm_rmsnorm_grad_args* a, rm_stream_t stream) {

@@ -21,23 +21,28 @@ __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x
 // the exponent and mantissa fields; 127 (scale 1) for a zero block, 255 (NaN)
 // for one with an infinity or a NaN.
 __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
-    if (amax >= 0x7f800000u) return 255u;
-    if (amax == 0u) return 127u;
-    const int b = (int)(amax >> 23) - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0);
-    return (uint32_t)max(b, 0);
+    // exponent field, plus one where the mantissa exceeds 1.75's, less 8
+    const int b = max((int)((amax + 0x1fffffu) >> 23) - 8, 0);
+    return amax >= 0x7f800000u ? 255u : amax == 0u ? 127u : (uint32_t)b;
 }
-// 2^-e of a scale byte other than 255: e = 127 at most is reached by no finite
-// fp32 block (byte <= 247), so the power is a normal number.
-__device__ __forceinline__ float scale_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+// 2^-e of a scale byte as a float: a normal number for every finite block
+// (byte <= 247), and NaN for byte 255, which makes the block's codes NaN.
+__device__ __forceinline__ float scale_inverse(uint32_t byte) {
+    return __uint_as_float(byte == 255u ? 0x7fffffffu : (254u - byte) << 23);
+}
 
-// Four e4m3 codes (nearest even; |x * inv| <= 448 by the choice of the scale,
-// the saturation only meets NaN blocks, whose codes the caller replaces).
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-    return lo | (hi << 16);
+// Largest of magnitudes, NaN if any is.
+__device__ __forceinline__ float max_abs(float m, float2 v) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(v.x)), "f"(fabsf(v.y)));
+    return r;
 }
-constexpr uint32_t kNanCodes = 0x7f7f7f7fu;
+
+// Four e4m3 codes, nearest even; |x * inv| <= 448 by the choice of the scale.
+__device__ __forceinline__ uint32_t e4m3x4(float2 a, float2 b) {
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3) |
+           ((uint32_t)__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3) << 16);
+}
 
 // ------------------------------------------------------------- tensor cores
 // Instruction descriptor of kind::mxf8f6f4: e4m3 A and B (format code 0), both
@@ -162,5 +167,20 @@ template <int N>
 __device__ __forceinline__ void bulk_wait_read() {
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
+
+// The opt-in to more than 48 KB of shared memory, once per kernel and device.
+struct SmemGrant {
+    bool done[64] = {};
+    template <typename F>
+    cudaError_t ask(F* kernel, int bytes) {
+        int d = 0;
+        cudaError_t e = cudaGetDevice(&d);
+        if (e != cudaSuccess || (d < 64 && __atomic_load_n(&done[d], __ATOMIC_ACQUIRE))) return e;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess && d < 64) __atomic_store_n(&done[d], true, __ATOMIC_RELEASE);
+        return e;
+    }
+};
+
 
 }  // namespace rm

@@ -28,16 +28,34 @@ __device__ __forceinline__ uint32_t max16(uint32_t m) {   // over the 16 lanes o
     return m;
 }
 
+// 8 x 8 elements as they were loaded, and the largest magnitude bits of a row,
+// of columns, of all (ordered like the magnitudes, NaN on top).
 template <typename E>
-struct Patch;   // 8 x 8 elements as they were loaded
+struct Patch;
 template <>
 struct Patch<__nv_bfloat16> {
     uint4 u[8];
     __device__ __forceinline__ void load(int r, const __nv_bfloat16* p) { u[r] = __ldcg(reinterpret_cast<const uint4*>(p)); }
     __device__ __forceinline__ void zero(int r) { u[r] = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ uint32_t word(int r, int i) const { return i == 0 ? u[r].x : i == 1 ? u[r].y : i == 2 ? u[r].z : u[r].w; }
     __device__ __forceinline__ float at(int r, int c) const {
-        const uint32_t w = c < 2 ? u[r].x : c < 4 ? u[r].y : c < 6 ? u[r].z : u[r].w;
+        const uint32_t w = word(r, c >> 1);
         return __uint_as_float(c & 1 ? w & 0xffff0000u : w << 16);
+    }
+    // two 16-bit magnitudes an instruction; as fp32 bits they are the high halves
+    __device__ __forceinline__ uint32_t row_max(int r) const {
+        const uint32_t m = __vmaxu2(__vmaxu2(u[r].x & 0x7fff7fffu, u[r].y & 0x7fff7fffu),
+                                    __vmaxu2(u[r].z & 0x7fff7fffu, u[r].w & 0x7fff7fffu));
+        return max(m << 16, m & 0xffff0000u);
+    }
+    __device__ __forceinline__ void col_max(uint32_t (&m)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t v = 0;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) v = __vmaxu2(v, word(r, i) & 0x7fff7fffu);
+            m[2 * i] = v << 16, m[2 * i + 1] = v & 0xffff0000u;
+        }
     }
 };
 template <>
@@ -52,12 +70,40 @@ struct Patch<float> {
         const float4 v = u[r][c >> 2];
         return (c & 3) == 0 ? v.x : (c & 3) == 1 ? v.y : (c & 3) == 2 ? v.z : v.w;
     }
+    __device__ __forceinline__ uint32_t row_max(int r) const {
+        uint32_t m = 0;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) m = max(m, abs_bits(at(r, c)));
+        return m;
+    }
+    __device__ __forceinline__ void col_max(uint32_t (&m)[8]) const {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            m[c] = 0;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) m[c] = max(m[c], abs_bits(at(r, c)));
+        }
+    }
 };
 
+// Codes of four elements of a block with 1 / scale = inv.
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float inv) {
+    return e4m3x4(f2_mul(make_float2(a, b), f2(inv)), f2_mul(make_float2(c, d), f2(inv)));
+}
+
+// 4 x 4 bytes turned: w[j] holds byte j of the four words.
+__device__ __forceinline__ void turn4(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t (&w)[4]) {
+    const uint32_t ab0 = __byte_perm(a, b, 0x5140), ab1 = __byte_perm(a, b, 0x7362);
+    const uint32_t cd0 = __byte_perm(c, d, 0x5140), cd1 = __byte_perm(c, d, 0x7362);
+    w[0] = __byte_perm(ab0, cd0, 0x5410), w[1] = __byte_perm(ab0, cd0, 0x7632);
+    w[2] = __byte_perm(ab1, cd1, 0x5410), w[3] = __byte_perm(ab1, cd1, 0x7632);
+}
+
 template <typename E, bool TILE>
-__global__ void __launch_bounds__(kThreads) quant_block_kernel(const QuantBlock p) {
+__global__ void __launch_bounds__(kThreads, sizeof(E) == 2 ? 4 : 2) quant_block_kernel(const QuantBlock p) {
     __shared__ uint32_t wmax[kThreads / 32];
-    __shared__ uint32_t cmax[kThreads / 32][kBlk];
+    __shared__ __align__(16) uint32_t cmax[kThreads / 32][kBlk];
+    __shared__ __align__(8) uint8_t cbyte[kBlk];
     __shared__ __align__(16) unsigned char turn[kBlk * kBlk];
     pdl_enter();
     const int tcol = (p.cols + kBlk - 1) / kBlk, trow = (p.rows + kBlk - 1) / kBlk;
@@ -81,9 +127,7 @@ __global__ void __launch_bounds__(kThreads) quant_block_kernel(const QuantBlock 
     if constexpr (TILE) {
         uint32_t m = 0;
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-#pragma unroll
-            for (int c = 0; c < 8; ++c) m = max(m, abs_bits(x.at(r, c)));
+        for (int r = 0; r < 8; ++r) m = max(m, x.row_max(r));
         m = __reduce_max_sync(0xffffffffu, m);
         if ((threadIdx.x & 31) == 0) wmax[warp] = m;
         __syncthreads();
@@ -96,70 +140,79 @@ __global__ void __launch_bounds__(kThreads) quant_block_kernel(const QuantBlock 
         }
     }
 
-    if (p.dst) {
+    uint2 q[8];   // codes of the patch's rows
+    if (TILE || p.dst) {
         uint8_t* dst = static_cast<uint8_t*>(p.dst) + g * p.dst_gs + (long long)r0 * p.dst_ld + c0;
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-            uint32_t b = tb;
-            if constexpr (!TILE) {
-                uint32_t m = 0;
-#pragma unroll
-                for (int c = 0; c < 8; ++c) m = max(m, abs_bits(x.at(r, c)));
-                b = scale_byte(max16(m));
+            const uint32_t b = TILE ? tb : scale_byte(max16(x.row_max(r)));
+            const float inv = scale_inverse(b);
+            q[r] = make_uint2(codes4(x.at(r, 0), x.at(r, 1), x.at(r, 2), x.at(r, 3), inv),
+                              codes4(x.at(r, 4), x.at(r, 5), x.at(r, 6), x.at(r, 7), inv));
+            if (p.dst && r0 + r < p.rows) {
+                if (cin) *reinterpret_cast<uint2*>(dst + (long long)r * p.dst_ld) = q[r];
+                if (!TILE && lane16 == 0) p.scale[g * p.s_gs + (r0 + r) * p.s_ld + cb] = (uint8_t)b;
             }
-            if (r0 + r >= p.rows) continue;   // (one row per half-warp; all shuffles of it are done)
-            const float inv = scale_inverse(min(b, 254u));
-            uint2 q = make_uint2(e4m3x4(x.at(r, 0) * inv, x.at(r, 1) * inv, x.at(r, 2) * inv, x.at(r, 3) * inv),
-                                 e4m3x4(x.at(r, 4) * inv, x.at(r, 5) * inv, x.at(r, 6) * inv, x.at(r, 7) * inv));
-            if (b == 255u) q = make_uint2(kNanCodes, kNanCodes);
-            if (cin) *reinterpret_cast<uint2*>(dst + (long long)r * p.dst_ld) = q;
-            if (!TILE && lane16 == 0) p.scale[g * p.s_gs + (r0 + r) * p.s_ld + cb] = (uint8_t)b;
         }
     }
 
     if (p.dst_t) {
-        uint32_t b[8];
-        if constexpr (TILE) {
+        // Column c of the patch: 8 bytes at slot pr of the column's 16 slots of
+        // shared memory, the slots permuted by the patch's column so that the 16
+        // lanes of a store meet 16 different bank pairs.
+        unsigned char* put = turn + 8 * lane16 * kBlk + ((pr ^ lane16) << 3);
+        if constexpr (TILE) {   // the same codes, turned
 #pragma unroll
-            for (int c = 0; c < 8; ++c) b[c] = tb;
+            for (int h = 0; h < 2; ++h) {
+                uint32_t lo[4], hi[4];
+                if (h == 0) {
+                    turn4(q[0].x, q[1].x, q[2].x, q[3].x, lo);
+                    turn4(q[4].x, q[5].x, q[6].x, q[7].x, hi);
+                } else {
+                    turn4(q[0].y, q[1].y, q[2].y, q[3].y, lo);
+                    turn4(q[4].y, q[5].y, q[6].y, q[7].y, hi);
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) *reinterpret_cast<uint2*>(put + (4 * h + c) * kBlk) = make_uint2(lo[c], hi[c]);
+            }
         } else {   // each column's largest magnitude over the tile's 128 rows
+            uint32_t m[8];
+            x.col_max(m);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                uint32_t m = 0;
-#pragma unroll
-                for (int r = 0; r < 8; ++r) m = max(m, abs_bits(x.at(r, c)));
-                m = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                if ((threadIdx.x & 31) < 16) cmax[warp][8 * lane16 + c] = m;
+            for (int c = 0; c < 8; ++c) m[c] = max(m[c], __shfl_xor_sync(0xffffffffu, m[c], 16));
+            if ((threadIdx.x & 31) < 16) {
+                *reinterpret_cast<uint4*>(&cmax[warp][8 * lane16]) = make_uint4(m[0], m[1], m[2], m[3]);
+                *reinterpret_cast<uint4*>(&cmax[warp][8 * lane16 + 4]) = make_uint4(m[4], m[5], m[6], m[7]);
             }
             __syncthreads();
+            if (threadIdx.x < kBlk) {   // one column a thread: its scale byte, for all
+                uint32_t v = 0;
+#pragma unroll
+                for (int w = 0; w < kThreads / 32; ++w) v = max(v, cmax[w][threadIdx.x]);
+                const uint32_t b = scale_byte(v);
+                cbyte[threadIdx.x] = (uint8_t)b;
+                const int col = cb * kBlk + threadIdx.x;
+                if (col < p.cols) p.scale_t[g * p.st_gs + col * p.st_ld + rb] = (uint8_t)b;
+            }
+            __syncthreads();
+            const uint2 b8 = *reinterpret_cast<const uint2*>(cbyte + 8 * lane16);
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-                uint32_t m = 0;
-#pragma unroll
-                for (int w = 0; w < kThreads / 32; ++w) m = max(m, cmax[w][8 * lane16 + c]);
-                b[c] = scale_byte(m);
-                if (pr == 0 && cin) p.scale_t[g * p.st_gs + (c0 + c) * p.st_ld + rb] = (uint8_t)b[c];
+                const uint32_t b = ((c < 4 ? b8.x : b8.y) >> (8 * (c & 3))) & 255u;
+                const float inv = scale_inverse(b);
+                uint2 w = make_uint2(codes4(x.at(0, c), x.at(1, c), x.at(2, c), x.at(3, c), inv),
+                                     codes4(x.at(4, c), x.at(5, c), x.at(6, c), x.at(7, c), inv));
+                *reinterpret_cast<uint2*>(put + c * kBlk) = w;
             }
-        }
-        // Column c of the patch: 8 bytes at slot pr of the column's 16 slots,
-        // the slots permuted by the patch's column so that the 16 lanes of a
-        // store meet 16 different bank pairs.
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            const float inv = scale_inverse(min(b[c], 254u));
-            uint2 q = make_uint2(e4m3x4(x.at(0, c) * inv, x.at(1, c) * inv, x.at(2, c) * inv, x.at(3, c) * inv),
-                                 e4m3x4(x.at(4, c) * inv, x.at(5, c) * inv, x.at(6, c) * inv, x.at(7, c) * inv));
-            if (b[c] == 255u) q = make_uint2(kNanCodes, kNanCodes);
-            *reinterpret_cast<uint2*>(turn + (8 * lane16 + c) * kBlk + ((pr ^ lane16) << 3)) = q;
         }
         __syncthreads();
         uint8_t* dst = static_cast<uint8_t*>(p.dst_t) + g * p.dt_gs;
 #pragma unroll
         for (int i = 0; i < kBlk * 8 / kThreads; ++i) {   // 16-byte pieces: 8 per column
-            const int k = threadIdx.x + i * kThreads, c = k >> 3, q = k & 7, sw = (c >> 3) & 15;
-            const int col = cb * kBlk + c, row = rb * kBlk + 16 * q;
+            const int k = threadIdx.x + i * kThreads, c = k >> 3, piece = k & 7, sw = (c >> 3) & 15;
+            const int col = cb * kBlk + c, row = rb * kBlk + 16 * piece;
             if (col >= p.cols || row >= p.rows) continue;
-            uint4 v = *reinterpret_cast<const uint4*>(turn + c * kBlk + (((2 * q) ^ (sw & 14)) << 3));
+            uint4 v = *reinterpret_cast<const uint4*>(turn + c * kBlk + (((2 * piece) ^ (sw & 14)) << 3));
             if (sw & 1) v = make_uint4(v.z, v.w, v.x, v.y);
             uint8_t* out = dst + (long long)col * p.dt_ld + row;
             if (row + 16 <= p.rows) {

@@ -8,11 +8,16 @@
 //     dx = rstd * (a - s * rstd^2 * mean(a * s)) + dsum
 //     dgamma = sum over rows of dy * s * rstd
 //
-// Both directions are bound by HBM: a row is read once into registers, the
-// statistics are fp32 sums, and everything leaves from the registers.  A row
-// belongs to TPR consecutive threads of a CTA, each holding NC chunks of 8
-// consecutive elements (one or two 16-byte loads), so a block of 128 is 16
-// neighbouring lanes and its largest magnitude costs four shuffles.
+// Both directions are bound by HBM: a row is read once and everything leaves
+// from the registers.  A row belongs to a group of threads (whole warps), each
+// with NC chunks of 8 consecutive elements, so a block of 128 is 16
+// neighbouring lanes and its largest magnitude costs four shuffles.  One CTA of
+// up to 512 threads an SM; its groups walk over the rows, the next rows on
+// their way into a ring in shared memory by cp.async: every thread copies the
+// chunks that it will read, so the ring needs no barrier, and what is in flight
+// (up to 200 KB an SM) depends neither on registers nor on where a group is in
+// its row.  With the rows loaded straight into registers, 16384 x 1536 ran at
+// 4.2-4.6 TB/s whatever the launch shape.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -22,315 +27,433 @@
 namespace rm {
 namespace {
 
-constexpr int kMinCta = 256;   // threads a CTA has at least (several rows for narrow ones)
+constexpr int kCta = 512;               // threads a CTA has at most
+constexpr int kRing = 200 * 1024;       // bytes of its ring
+constexpr int kSms = 148;
 
-// Eight consecutive elements as floats, and back (bf16 rounded to nearest even).
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 u = __ldcg(reinterpret_cast<const uint4*>(p));
-    float2 f[4];
-    unpack_pairs(u, f);
+// Eight consecutive elements as they lie in memory.
+template <typename E>
+struct Chunk {
+    static constexpr int N = sizeof(E) / 2;   // 16-byte pieces
+    uint4 u[N];
+    __device__ __forceinline__ void read(uint32_t shared) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[2 * i] = f[i].x, v[2 * i + 1] = f[i].y;
-}
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-    const float4 a = __ldcg(reinterpret_cast<const float4*>(p)), b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                              pack_bf16x2(v[6], v[7]));
-}
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-
-// Sum over the TPR threads of a row (every thread gets it).  red: one float
-// per warp of the CTA; all threads of the CTA call this together.
-template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float* red) {
-    v = warp_sum(v);
-    if constexpr (TPR > 32) {
-        const int warp = threadIdx.x >> 5;
-        if ((threadIdx.x & 31) == 0) red[warp] = v;
-        __syncthreads();
-        const float* r = red + warp / (TPR / 32) * (TPR / 32);
-        v = 0.f;
-#pragma unroll
-        for (int w = 0; w < TPR / 32; ++w) v += r[w];
+        for (int i = 0; i < N; ++i) u[i] = lds128(shared + 16 * i);
     }
-    return v;
+    __device__ __forceinline__ void store(void* base, long long at) const {
+        uint4* p = reinterpret_cast<uint4*>(static_cast<E*>(base) + at);
+#pragma unroll
+        for (int i = 0; i < N; ++i) p[i] = u[i];
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < N; ++i) u[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void set(const float2 (&v)[4]) {   // rounded to the type
+        if constexpr (N == 1) {
+            u[0] = pack_pairs(v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) u[i] = pack_pairs({v[2 * i], v[2 * i + 1]});
+        }
+    }
+    __device__ __forceinline__ void pairs(float2 (&v)[4]) const {
+        if constexpr (N == 1) {
+            unpack_pairs(u[0], v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                float2 h[2];
+                unpack_pairs(u[i], h);
+                v[2 * i] = h[0], v[2 * i + 1] = h[1];
+            }
+        }
+    }
+};
+__device__ __forceinline__ void load_params(const float* p, float2 (&g)[4]) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    g[0] = make_float2(a.x, a.y), g[1] = make_float2(a.z, a.w), g[2] = make_float2(b.x, b.y), g[3] = make_float2(b.z, b.w);
+}
+// 1 / sqrt(x): the approximation (2^-22.9) and a Newton step.
+__device__ __forceinline__ float inv_sqrt(float x) {
+    const float r = rsqrtf(x);
+    const float c = fmaf(-0.5f * x * r, r, 0.5f);
+    return isinf(r) || r == 0.f ? r : fmaf(r, c, r);
 }
 
-template <typename E, int TPR, int NC>
-__global__ void __launch_bounds__(TPR > kMinCta ? TPR : kMinCta) rmsnorm_kernel(const RmsNorm p) {
-    constexpr int CTA = TPR > kMinCta ? TPR : kMinCta;
-    __shared__ float red[CTA / 32];
+// One chunk (8 elements) of a global row into shared memory, asynchronously.
+template <typename E>
+__device__ __forceinline__ void copy_chunk(uint32_t dst, const void* base, long long at) {
+    const char* src = reinterpret_cast<const char*>(static_cast<const E*>(base) + at);
+#pragma unroll
+    for (int i = 0; i < Chunk<E>::N; ++i)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 16 * i), "l"(src + 16 * i) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Wait for all but this thread's last n groups of copies.
+__device__ __forceinline__ void copies_wait(int n) {
+    switch (n) {
+        case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+        case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+        case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    }
+}
+
+// A thread's place: its group (row) of the CTA and its rank there.
+struct Place {
+    int tpr, group, groups, t, first_warp, warps;
+    __device__ __forceinline__ explicit Place(int tpr_) : tpr(tpr_) {
+        groups = blockDim.x / tpr;
+        group = threadIdx.x / tpr;
+        t = threadIdx.x - group * tpr;
+        warps = tpr >> 5;
+        first_warp = group * warps;
+    }
+    // Sum over the group's threads (every thread gets it), in a fixed order.
+    // red: a float per warp of the CTA, not the last call's; all threads of the
+    // group call this together.
+    __device__ __forceinline__ float sum(float v, float* red) const {
+        v = warp_sum(v);
+        if (warps > 1) {
+            if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(tpr) : "memory");
+            v = 0.f;
+            for (int w = 0; w < warps; ++w) v += red[first_warp + w];
+        }
+        return v;
+    }
+};
+
+template <typename E, int NC, bool RESID>
+__global__ void __launch_bounds__(kCta, 1) rmsnorm_kernel(const RmsNorm p, int tpr, int stages) {
+    __shared__ float red[2][kCta / 32];
+    extern __shared__ __align__(16) unsigned char ring[];
     pdl_enter();
-    const int t = threadIdx.x % TPR;
-    const long long row = (long long)blockIdx.x * (CTA / TPR) + threadIdx.x / TPR;
-    const bool live = row < p.rows;
+    const Place at(tpr);
     const int nch = p.D / 8;
-    float v[NC][8];
-    float ss = 0.f;
+    const float inv_d = 1.0f / (float)p.D;
+    const uint32_t bytes = (uint32_t)(p.D * sizeof(E)), slot = bytes * (RESID ? 2 : 1);
+    const uint32_t mine = smem_u32(ring) + (uint32_t)(at.group * stages) * slot + (uint32_t)at.t * 8 * sizeof(E);
+    const uint32_t hop = (uint32_t)tpr * 8 * sizeof(E);   // from a thread's chunk to its next
+    const long long step = (long long)gridDim.x * at.groups;
+    long long row = (long long)blockIdx.x * at.groups + at.group;
+    auto fetch = [&](long long r, int s) {
+        if (r < p.rows) {
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        const int c = t + i * TPR;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
-        if (live && c < nch) load8(static_cast<const E*>(p.X) + row * p.ld_x + 8 * c, v[i]);
-    }
-    if (p.R) {
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int c = t + i * TPR;
-            if (live && c < nch) {
-                float r[8];
-                load8(static_cast<const E*>(p.R) + row * p.ld_r + 8 * c, r);
-                // the stream is rounded to its type here: the statistics, the
-                // output and the gradient all see the values that are stored
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[i][e] = to_f(from_f<E>(v[i][e] + r[e]));
-            }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        const int c = t + i * TPR;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(v[i][e], v[i][e], ss);
-        if (p.Sum && live && c < nch) store8(static_cast<E*>(p.Sum) + row * p.ld_sum + 8 * c, v[i]);
-    }
-    ss = row_sum<TPR>(ss, red);
-    const float rstd = 1.0f / sqrtf(ss / (float)p.D + p.eps);
-    if (!live) return;
-    if (p.rstd && t == 0) p.rstd[row] = rstd;
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        const int c = t + i * TPR;
-        const bool in = c < nch;
-        float y[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = v[i][e] * rstd;
-        if (in && p.gamma) {
-            const float4 a = reinterpret_cast<const float4*>(p.gamma + 8 * c)[0];
-            const float4 b = reinterpret_cast<const float4*>(p.gamma + 8 * c)[1];
-            y[0] *= a.x, y[1] *= a.y, y[2] *= a.z, y[3] *= a.w, y[4] *= b.x, y[5] *= b.y, y[6] *= b.z, y[7] *= b.w;
-        }
-        if (in && p.Y) store8(static_cast<E*>(p.Y) + row * p.ld_y + 8 * c, y);
-        if (p.Yq) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) m = max(m, abs_bits(y[e]));   // (zero past the row's end)
-            // TPR is a multiple of 32 and `live` is one value per row: whole
-            // half-warps take part
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const uint32_t b = scale_byte(m);
-            const float inv = scale_inverse(min(b, 254u));
-            if (in) {
-                uint2 q = make_uint2(e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
-                                     e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
-                if (b == 255u) q = make_uint2(kNanCodes, kNanCodes);
-                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.Yq) + row * p.ld_yq + 8 * c) = q;
-                if ((threadIdx.x & 15) == 0) p.Ys[row * p.ld_ys + c / 16] = (uint8_t)b;
-            }
-        }
-    }
-}
-
-// Gradient: a CTA walks rows (grid-stride) and keeps its columns' sums of
-// dy * s * rstd in registers; they leave as one partial row per CTA.
-template <typename E, int TPR, int NC>
-__global__ void __launch_bounds__(TPR > kMinCta ? TPR : kMinCta) rmsnorm_bwd_kernel(const RmsNormGrad p) {
-    constexpr int CTA = TPR > kMinCta ? TPR : kMinCta;
-    constexpr int RPC = CTA / TPR;
-    __shared__ float red[2][CTA / 32];
-    extern __shared__ float acc_s[];   // [D]: the CTA's column sums (RPC > 1)
-    pdl_enter();
-    const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
-    const int nch = p.D / 8;
-    float g[NC][8], acc[NC][8];
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        const int c = t + i * TPR;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            acc[i][e] = 0.f;
-            g[i][e] = 1.f;
-        }
-        if (p.gamma && c < nch) {
-            const float* q = p.gamma + 8 * c;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) g[i][e] = q[e];
-        }
-    }
-    int par = 0;
-    for (long long r0 = (long long)blockIdx.x * RPC; r0 < p.rows; r0 += (long long)gridDim.x * RPC, par ^= 1) {
-        const long long row = r0 + grp;
-        const bool live = row < p.rows;
-        float s[NC][8], a[NC][8];
-        float dot = 0.f;
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int c = t + i * TPR;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s[i][e] = a[i][e] = 0.f;
-            if (live && c < nch) {
-                load8(static_cast<const E*>(p.S) + row * p.ld_s + 8 * c, s[i]);
-                load8(static_cast<const E*>(p.dY) + row * p.ld_dy + 8 * c, a[i]);
-            }
-        }
-        const float rstd = live ? __ldcg(p.rstd + row) : 0.f;
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                acc[i][e] = fmaf(a[i][e] * rstd, s[i][e], acc[i][e]);
-                a[i][e] *= g[i][e];
-                dot = fmaf(a[i][e], s[i][e], dot);
-            }
-        }
-        dot = row_sum<TPR>(dot, red[par]);
-        const float k = -rstd * rstd * (dot / (float)p.D);
-        if (!live) continue;
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int c = t + i * TPR;
-            if (c < nch) {
-                float d[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) d[e] = rstd * fmaf(s[i][e], k, a[i][e]);
-                if (p.dSum) {
-                    float u[8];
-                    load8(static_cast<const E*>(p.dSum) + row * p.ld_dsum + 8 * c, u);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) d[e] += u[e];
+            for (int i = 0; i < NC; ++i) {
+                const int c = at.t + i * tpr;
+                if (c < nch) {
+                    copy_chunk<E>(mine + s * slot + i * hop, p.X, r * p.ld_x + 8 * c);
+                    if constexpr (RESID) copy_chunk<E>(mine + s * slot + bytes + i * hop, p.R, r * p.ld_r + 8 * c);
                 }
-                store8(static_cast<E*>(p.dX) + row * p.ld_dx + 8 * c, d);
             }
         }
+        copies_commit();
+    };
+    for (int s = 0; s < stages - 1; ++s) fetch(row + s * step, s);
+    int s = 0, last = stages - 1;   // the ring's place of this row and of the row stages - 1 on
+    for (int par = 0; row < p.rows; row += step, par ^= 1) {   // (one value of row per group)
+        fetch(row + (stages - 1) * step, last);
+        copies_wait(stages - 1);
+        Chunk<E> x[NC];
+        float2 sq = f2(0.f);
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int c = at.t + i * tpr;
+            if (c < nch) {
+                float2 v[4];
+                x[i].read(mine + s * slot + i * hop);
+                x[i].pairs(v);
+                if constexpr (RESID) {
+                    // the stream is rounded to its type here: the statistics, the
+                    // output and the gradient all see the values that are stored
+                    Chunk<E> r;
+                    float2 q[4];
+                    r.read(mine + s * slot + bytes + i * hop);
+                    r.pairs(q);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = f2_add(v[e], q[e]);
+                    x[i].set(v);
+                    x[i].pairs(v);
+                }
+                if (p.Sum) x[i].store(p.Sum, row * p.ld_sum + 8 * c);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sq = f2_fma(v[e], v[e], sq);
+            } else {
+                x[i].clear();
+            }
+        }
+        last = s;
+        s = s + 1 == stages ? 0 : s + 1;
+        const float rstd = inv_sqrt(fmaf(at.sum(sq.x + sq.y, red[par]), inv_d, p.eps));
+        if (p.rstd && at.t == 0) p.rstd[row] = rstd;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int c = at.t + i * tpr;
+            const bool in = c < nch;
+            float2 y[4];
+            x[i].pairs(y);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = f2_mul(y[e], f2(rstd));
+            if (in && p.gamma) {
+                float2 g[4];
+                load_params(p.gamma + 8 * c, g);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = f2_mul(y[e], g[e]);
+            }
+            if (in && p.Y) {
+                Chunk<E> o;
+                o.set(y);
+                o.store(p.Y, row * p.ld_y + 8 * c);
+            }
+            if (p.Yq) {   // (whole warps: tpr is a multiple of 32)
+                float mf = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mf = max_abs(mf, y[e]);
+                uint32_t m = in ? abs_bits(mf) : 0u;
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                const uint32_t b = scale_byte(m);
+                const float2 inv = f2(scale_inverse(b));
+                if (in) {
+                    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.Yq) + row * p.ld_yq + 8 * c) =
+                        make_uint2(e4m3x4(f2_mul(y[0], inv), f2_mul(y[1], inv)), e4m3x4(f2_mul(y[2], inv), f2_mul(y[3], inv)));
+                    if ((threadIdx.x & 15) == 0) p.Ys[row * p.ld_ys + c / 16] = (uint8_t)b;
+                }
+            }
+        }
+    }
+}
+
+// Gradient: the groups keep their columns' sums of dy * s * rstd in registers;
+// a CTA's groups add theirs in order and leave one partial row.
+template <typename E, int NC>
+__global__ void __launch_bounds__(kCta, 1) rmsnorm_bwd_kernel(const RmsNormGrad p, int tpr, int stages) {
+    __shared__ float red[2][kCta / 32];
+    extern __shared__ __align__(16) unsigned char ring[];
+    pdl_enter();
+    const Place at(tpr);
+    const int nch = p.D / 8;
+    const uint32_t bytes = (uint32_t)(p.D * sizeof(E)), slot = bytes * (p.dSum ? 3 : 2);
+    const uint32_t mine = smem_u32(ring) + (uint32_t)(at.group * stages) * slot + (uint32_t)at.t * 8 * sizeof(E);
+    const uint32_t hop = (uint32_t)tpr * 8 * sizeof(E);
+    const float inv_d = 1.0f / (float)p.D;
+    float2 acc[NC][4];
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][e] = f2(0.f);
+    const long long step = (long long)gridDim.x * at.groups;
+    long long row = (long long)blockIdx.x * at.groups + at.group;
+    auto fetch = [&](long long r, int s) {
+        if (r < p.rows) {
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const int c = at.t + i * tpr;
+                if (c < nch) {
+                    const uint32_t d = mine + s * slot + i * hop;
+                    copy_chunk<E>(d, p.S, r * p.ld_s + 8 * c);
+                    copy_chunk<E>(d + bytes, p.dY, r * p.ld_dy + 8 * c);
+                    if (p.dSum) copy_chunk<E>(d + 2 * bytes, p.dSum, r * p.ld_dsum + 8 * c);
+                }
+            }
+        }
+        copies_commit();
+    };
+    for (int s = 0; s < stages - 1; ++s) fetch(row + s * step, s);
+    int s = 0, last = stages - 1;
+    float rstd = row < p.rows ? __ldcg(p.rstd + row) : 0.f;
+    for (int par = 0; row < p.rows; row += step, par ^= 1) {
+        fetch(row + (stages - 1) * step, last);
+        const float next_rstd = row + step < p.rows ? __ldcg(p.rstd + row + step) : 0.f;
+        copies_wait(stages - 1);
+        float2 dots = f2(0.f);
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int c = at.t + i * tpr;
+            if (c < nch) {
+                Chunk<E> cs, cy;
+                float2 sv[4], dy[4];
+                cs.read(mine + s * slot + i * hop);
+                cy.read(mine + s * slot + i * hop + bytes);
+                cs.pairs(sv);
+                cy.pairs(dy);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][e] = f2_fma(f2_mul(dy[e], f2(rstd)), sv[e], acc[i][e]);
+                if (p.gamma) {
+                    float2 g[4];
+                    load_params(p.gamma + 8 * c, g);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dy[e] = f2_mul(dy[e], g[e]);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dots = f2_fma(dy[e], sv[e], dots);
+            }
+        }
+        const float dot = at.sum(dots.x + dots.y, red[par]);
+        const float2 k = f2(-rstd * rstd * (dot * inv_d));
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int c = at.t + i * tpr;
+            if (c < nch) {
+                Chunk<E> cs, cy;
+                float2 sv[4], dy[4];
+                cs.read(mine + s * slot + i * hop);
+                cy.read(mine + s * slot + i * hop + bytes);
+                cs.pairs(sv);
+                cy.pairs(dy);
+                if (p.gamma) {
+                    float2 g[4];
+                    load_params(p.gamma + 8 * c, g);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dy[e] = f2_mul(dy[e], g[e]);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dy[e] = f2_mul(f2_fma(sv[e], k, dy[e]), f2(rstd));
+                if (p.dSum) {
+                    cs.read(mine + s * slot + i * hop + 2 * bytes);
+                    cs.pairs(sv);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dy[e] = f2_add(dy[e], sv[e]);
+                }
+                cs.set(dy);
+                cs.store(p.dX, row * p.ld_dx + 8 * c);
+            }
+        }
+        last = s;
+        s = s + 1 == stages ? 0 : s + 1;
+        rstd = next_rstd;
     }
     if (!p.part) return;
-    if constexpr (RPC > 1) {   // the CTA's rows in a fixed order
-        for (int k = 0; k < RPC; ++k) {
-            __syncthreads();
-            if (grp == k) {
+    // (every group has finished its rows: the ring now carries the sums from
+    // group to group)
+    float* acc_s = reinterpret_cast<float*>(ring);
+    for (int k = 0; k < at.groups; ++k) {
+        __syncthreads();
+        if (at.group == k) {
 #pragma unroll
-                for (int i = 0; i < NC; ++i) {
-                    const int c = t + i * TPR;
-                    if (c < nch)
+            for (int i = 0; i < NC; ++i) {
+                const int c = at.t + i * tpr;
+                if (c < nch) {
+                    float2* a = reinterpret_cast<float2*>(acc_s + 8 * c);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            if (k) acc[i][e] += acc_s[8 * c + e];
-                            if (k < RPC - 1) acc_s[8 * c + e] = acc[i][e];
-                        }
+                    for (int e = 0; e < 4; ++e) {
+                        if (k) acc[i][e] = f2_add(acc[i][e], a[e]);
+                        if (k < at.groups - 1) a[e] = acc[i][e];
+                    }
+                    if (k == at.groups - 1) {
+                        Chunk<float> o;
+                        o.set(acc[i]);
+                        o.store(p.part, (long long)blockIdx.x * p.D + 8 * c);
+                    }
                 }
             }
-        }
-    }
-    if (grp == RPC - 1) {
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int c = t + i * TPR;
-            if (c < nch) store8(p.part + (long long)blockIdx.x * p.D + 8 * c, acc[i]);
         }
     }
 }
 
 // dgamma[d] = sum over the partial rows, in a fixed order: 32 columns a CTA,
-// 32 warps taking every 32nd row, then the warps' sums.
+// 32 warps taking every 32nd row (eight loads in flight), then the warps' sums.
 __global__ void __launch_bounds__(1024) colsum_parts_kernel(const float* part, float* out, int parts, int D) {
     __shared__ float s[32][33];
     pdl_enter();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int d = blockIdx.x * 32 + lane;
     float v = 0.f;
-    if (d < D)
-        for (int r = warp; r < parts; r += 32) v += __ldcg(part + (long long)r * D + d);
+    if (d < D) {
+        for (int r0 = warp; r0 < parts; r0 += 32 * 8) {
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = r0 + 32 * j < parts ? __ldcg(part + (long long)(r0 + 32 * j) * D + d) : 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v += x[j];
+        }
+    }
     s[warp][lane] = v;
     __syncthreads();
     v = warp_sum(s[lane][warp]);
     if (lane == 0 && blockIdx.x * 32 + warp < D) out[blockIdx.x * 32 + warp] = v;
 }
 
-// Threads per row: the fewest (of 32 .. 512) that hold the row in at most
-// `most` chunks each.
-int pick_tpr(int D, int most) {
-    int tpr = 32;
-    while (tpr < 512 && (D / 8 + tpr - 1) / tpr > most) tpr *= 2;
-    return tpr;
-}
-
-template <typename E, int TPR, int NC>
-cudaError_t fwd(const RmsNorm& p, cudaStream_t s) {
-    const int rpc = TPR > kMinCta ? 1 : kMinCta / TPR;
-    return launch_pdl(rmsnorm_kernel<E, TPR, NC>, dim3((unsigned)((p.rows + rpc - 1) / rpc)), dim3(rpc * TPR), 0, s, p);
-}
-template <typename E, int TPR>
-cudaError_t fwd_nc(const RmsNorm& p, cudaStream_t s) {
-    switch ((p.D / 8 + TPR - 1) / TPR) {
-        case 1: return fwd<E, TPR, 1>(p, s);
-        case 2: return fwd<E, TPR, 2>(p, s);
-        case 3: return fwd<E, TPR, 3>(p, s);
-        case 4: return fwd<E, TPR, 4>(p, s);
-        default: return cudaErrorInvalidValue;
+// Launch shape for rows of D whose `row_bytes` (all inputs) go through the ring.
+struct Shape {
+    int nc, tpr, groups, threads, stages, grid;
+    size_t smem;
+    Shape(long long rows, int D, size_t row_bytes) {
+        const int nch = D / 8;
+        // Warps a row: as few as hold it in six chunks a thread (what a row costs
+        // besides, its sum and its waits, is then shared by 48 elements a thread),
+        // but all of them where the SMs have a row each.
+        const int most = (nch + 31) / 32;
+        int w = rows <= kSms ? most : (most + 5) / 6;
+        w = std::min(w, kCta / 32);
+        tpr = 32 * w;
+        nc = (nch + tpr - 1) / tpr;
+        groups = kCta / tpr;
+        if (tpr > 32) groups = std::min(groups, 15);   // (named barriers)
+        groups = (int)std::min<long long>(groups, (rows + kSms - 1) / kSms);
+        groups = (int)std::min<size_t>(groups, kRing / row_bytes);
+        stages = (int)std::min<size_t>(4, kRing / (row_bytes * groups));
+        threads = groups * tpr;
+        smem = row_bytes * groups * stages;
+        grid = (int)std::min<long long>((rows + groups - 1) / groups, kSms);
     }
+};
+
+template <typename E, int NC, bool RESID>
+cudaError_t fwd(const RmsNorm& p, const Shape& sh, cudaStream_t s) {
+    static SmemGrant grant;
+    if (cudaError_t e = grant.ask(rmsnorm_kernel<E, NC, RESID>, kRing)) return e;
+    return launch_pdl(rmsnorm_kernel<E, NC, RESID>, dim3(sh.grid), dim3(sh.threads), sh.smem, s, p, sh.tpr, sh.stages);
 }
-template <typename E>
+template <typename E, bool RESID>
 cudaError_t fwd_e(const RmsNorm& p, cudaStream_t s) {
-    switch (pick_tpr(p.D, 4)) {
-        case 32: return fwd_nc<E, 32>(p, s);
-        case 64: return fwd_nc<E, 64>(p, s);
-        case 128: return fwd_nc<E, 128>(p, s);
-        case 256: return fwd_nc<E, 256>(p, s);
-        default: return fwd_nc<E, 512>(p, s);
+    const Shape sh(p.rows, p.D, sizeof(E) * p.D * (RESID ? 2 : 1));
+    switch (sh.nc) {
+        case 1: return fwd<E, 1, RESID>(p, sh, s);
+        case 2: return fwd<E, 2, RESID>(p, sh, s);
+        case 3: return fwd<E, 3, RESID>(p, sh, s);
+        case 4: return fwd<E, 4, RESID>(p, sh, s);
+        case 5: return fwd<E, 5, RESID>(p, sh, s);
+        default: return fwd<E, 6, RESID>(p, sh, s);
     }
 }
 
-template <typename E, int TPR, int NC>
-cudaError_t bwd(const RmsNormGrad& p, int grid, cudaStream_t s) {
-    constexpr int rpc = TPR > kMinCta ? 1 : kMinCta / TPR;
-    const size_t smem = rpc > 1 && p.part ? sizeof(float) * p.D : 0;   // (TPR < 256: D <= 4096, 16 KB)
-    return launch_pdl(rmsnorm_bwd_kernel<E, TPR, NC>, dim3(grid), dim3(rpc * TPR), smem, s, p);
+template <typename E, int NC>
+cudaError_t bwd(const RmsNormGrad& p, const Shape& sh, cudaStream_t s) {
+    static SmemGrant grant;
+    if (cudaError_t e = grant.ask(rmsnorm_bwd_kernel<E, NC>, kRing)) return e;
+    return launch_pdl(rmsnorm_bwd_kernel<E, NC>, dim3(sh.grid), dim3(sh.threads), sh.smem, s, p, sh.tpr, sh.stages);
 }
-template <typename E, int TPR>
-cudaError_t bwd_nc(const RmsNormGrad& p, int grid, cudaStream_t s) {
-    switch ((p.D / 8 + TPR - 1) / TPR) {
-        case 1: return bwd<E, TPR, 1>(p, grid, s);
-        case 2: return bwd<E, TPR, 2>(p, grid, s);
-        case 3: return bwd<E, TPR, 3>(p, grid, s);
-        case 4: return bwd<E, TPR, 4>(p, grid, s);
-        default: return cudaErrorInvalidValue;
-    }
-}
+
 template <typename E>
-cudaError_t bwd_e(const RmsNormGrad& p, int tpr, int grid, cudaStream_t s) {
-    switch (tpr) {
-        case 32: return bwd_nc<E, 32>(p, grid, s);
-        case 64: return bwd_nc<E, 64>(p, grid, s);
-        case 128: return bwd_nc<E, 128>(p, grid, s);
-        case 256: return bwd_nc<E, 256>(p, grid, s);
-        default: return bwd_nc<E, 512>(p, grid, s);
+cudaError_t bwd_e(const RmsNormGrad& p, const Shape& sh, cudaStream_t s) {
+    switch (sh.nc) {
+        case 1: return bwd<E, 1>(p, sh, s);
+        case 2: return bwd<E, 2>(p, sh, s);
+        case 3: return bwd<E, 3>(p, sh, s);
+        case 4: return bwd<E, 4>(p, sh, s);
+        case 5: return bwd<E, 5>(p, sh, s);
+        default: return bwd<E, 6>(p, sh, s);
     }
 }
 
 }  // namespace
 
 cudaError_t launch_rmsnorm(int dtype, const RmsNorm& p, cudaStream_t s) {
-    return dtype == RM_BF16 ? fwd_e<__nv_bfloat16>(p, s) : fwd_e<float>(p, s);
+    if (dtype == RM_BF16) return p.R ? fwd_e<__nv_bfloat16, true>(p, s) : fwd_e<__nv_bfloat16, false>(p, s);
+    return p.R ? fwd_e<float, true>(p, s) : fwd_e<float, false>(p, s);
 }
 
-int rmsnorm_bwd_parts(long long rows, int D) {
-    const int tpr = pick_tpr(D, 4), rpc = tpr > kMinCta ? 1 : kMinCta / tpr;
-    return (int)std::min<long long>((rows + rpc - 1) / rpc, 592);
-}
+// Partial rows of the column sums: one a CTA, one CTA an SM.
+int rmsnorm_bwd_parts(long long rows) { return (int)std::min<long long>(rows, kSms); }
 
 cudaError_t launch_rmsnorm_bwd(int dtype, const RmsNormGrad& p, float* dgamma, cudaStream_t s) {
-    const int tpr = pick_tpr(p.D, 4), grid = rmsnorm_bwd_parts(p.rows, p.D);
-    cudaError_t e = dtype == RM_BF16 ? bwd_e<__nv_bfloat16>(p, tpr, grid, s) : bwd_e<float>(p, tpr, grid, s);
+    const Shape sh(p.rows, p.D, (dtype == RM_BF16 ? 2 : 4) * (size_t)p.D * (p.dSum ? 3 : 2));
+    const cudaError_t e = dtype == RM_BF16 ? bwd_e<__nv_bfloat16>(p, sh, s) : bwd_e<float>(p, sh, s);
     if (e != cudaSuccess || !dgamma) return e;
-    return launch_pdl(colsum_parts_kernel, dim3((p.D + 31) / 32), dim3(1024), 0, s, (const float*)p.part, dgamma, grid,
+    return launch_pdl(colsum_parts_kernel, dim3((p.D + 31) / 32), dim3(1024), 0, s, (const float*)p.part, dgamma, sh.grid,
                       p.D);
 }
 
