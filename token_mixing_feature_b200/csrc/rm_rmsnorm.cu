@@ -8,16 +8,16 @@
 //     dx = rstd * (a - s * rstd^2 * mean(a * s)) + dsum
 //     dgamma = sum over rows of dy * s * rstd
 //
-// Both directions are bound by HBM: a row is read once and everything leaves
-// from the registers.  A row belongs to a group of threads (whole warps), each
-// with NC chunks of 8 consecutive elements, so a block of 128 is 16
-// neighbouring lanes and its largest magnitude costs four shuffles.  One CTA of
-// up to 512 threads an SM; its groups walk over the rows, the next rows on
-// their way into a ring in shared memory by cp.async: every thread copies the
-// chunks that it will read, so the ring needs no barrier, and what is in flight
-// (up to 200 KB an SM) depends neither on registers nor on where a group is in
-// its row.  With the rows loaded straight into registers, 16384 x 1536 ran at
-// 4.2-4.6 TB/s whatever the launch shape.
+// Both directions are bound by HBM and, next, by the instructions an element
+// takes.  A row belongs to a group of whole warps, warp w holding the NC * 32
+// chunks of 16 bytes from w * NC * 32 on, chunk 32 i + lane in lane `lane`: the
+// i-th chunks' addresses differ by constants, and a block of 128 is 16 (bf16) or
+// 32 (fp32) neighbouring lanes.  One CTA of up to 512 threads an SM; its groups walk over
+// the rows, the next ones on their way into a ring in shared memory by cp.async:
+// every thread copies the chunks that it will read, so the ring needs no
+// barrier, and what is in flight (up to 220 KB an SM) depends neither on
+// registers nor on where a group is in its row.  With the rows loaded straight
+// into registers, 16384 x 1536 ran at 4.2-4.6 TB/s whatever the launch shape.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -28,51 +28,35 @@ namespace rm {
 namespace {
 
 constexpr int kCta = 512;               // threads a CTA has at most
-constexpr int kRing = 200 * 1024;       // bytes of its ring
+constexpr int kRing = 222 * 1024;       // bytes of its ring, gamma included
 constexpr int kSms = 148;
 
-// Eight consecutive elements as they lie in memory.
+// 16 bytes of a row as they lie in memory: CE elements, as P pairs of floats.
+// A block of 128 is LANES neighbouring lanes' chunks.
 template <typename E>
 struct Chunk {
-    static constexpr int N = sizeof(E) / 2;   // 16-byte pieces
-    uint4 u[N];
-    __device__ __forceinline__ void read(uint32_t shared) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) u[i] = lds128(shared + 16 * i);
-    }
-    __device__ __forceinline__ void store(void* base, long long at) const {
-        uint4* p = reinterpret_cast<uint4*>(static_cast<E*>(base) + at);
-#pragma unroll
-        for (int i = 0; i < N; ++i) p[i] = u[i];
-    }
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int i = 0; i < N; ++i) u[i] = make_uint4(0u, 0u, 0u, 0u);
-    }
-    __device__ __forceinline__ void set(const float2 (&v)[4]) {   // rounded to the type
-        if constexpr (N == 1) {
-            u[0] = pack_pairs(v);
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) u[i] = pack_pairs({v[2 * i], v[2 * i + 1]});
-        }
-    }
-    __device__ __forceinline__ void pairs(float2 (&v)[4]) const {
-        if constexpr (N == 1) {
-            unpack_pairs(u[0], v);
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                float2 h[2];
-                unpack_pairs(u[i], h);
-                v[2 * i] = h[0], v[2 * i + 1] = h[1];
-            }
-        }
-    }
+    static constexpr int CE = 16 / sizeof(E), P = CE / 2, LANES = 128 / CE;
+    uint4 u;
+    __device__ __forceinline__ void read(uint32_t shared) { u = lds128(shared); }
+    __device__ __forceinline__ void store(char* p) const { *reinterpret_cast<uint4*>(p) = u; }
+    __device__ __forceinline__ void clear() { u = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void set(const float2 (&v)[P]) { u = pack_pairs(v); }   // rounded to the type
+    __device__ __forceinline__ void pairs(float2 (&v)[P]) const { unpack_pairs(u, v); }
 };
-__device__ __forceinline__ void load_params(const float* p, float2 (&g)[4]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    g[0] = make_float2(a.x, a.y), g[1] = make_float2(a.z, a.w), g[2] = make_float2(b.x, b.y), g[3] = make_float2(b.z, b.w);
+template <int P>
+__device__ __forceinline__ void load_params(const float* p, float2 (&g)[P]) {
+#pragma unroll
+    for (int i = 0; i < P; i += 2) {
+        const float4 a = reinterpret_cast<const float4*>(p)[i / 2];
+        g[i] = make_float2(a.x, a.y), g[i + 1] = make_float2(a.z, a.w);
+    }
+}
+// Codes of a chunk with 1 / scale = k, stored.
+__device__ __forceinline__ void store_codes(char* o, const float2 (&y)[4], float2 k) {
+    *reinterpret_cast<uint2*>(o) = make_uint2(e4m3x4(f2_mul(y[0], k), f2_mul(y[1], k)), e4m3x4(f2_mul(y[2], k), f2_mul(y[3], k)));
+}
+__device__ __forceinline__ void store_codes(char* o, const float2 (&y)[2], float2 k) {
+    *reinterpret_cast<uint32_t*>(o) = e4m3x4(f2_mul(y[0], k), f2_mul(y[1], k));
 }
 // 1 / sqrt(x): the approximation (2^-22.9) and a Newton step.
 __device__ __forceinline__ float inv_sqrt(float x) {
@@ -81,13 +65,9 @@ __device__ __forceinline__ float inv_sqrt(float x) {
     return isinf(r) || r == 0.f ? r : fmaf(r, c, r);
 }
 
-// One chunk (8 elements) of a global row into shared memory, asynchronously.
-template <typename E>
-__device__ __forceinline__ void copy_chunk(uint32_t dst, const void* base, long long at) {
-    const char* src = reinterpret_cast<const char*>(static_cast<const E*>(base) + at);
-#pragma unroll
-    for (int i = 0; i < Chunk<E>::N; ++i)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 16 * i), "l"(src + 16 * i) : "memory");
+// One chunk of a global row into shared memory, asynchronously.
+__device__ __forceinline__ void copy_chunk(uint32_t dst, const char* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Wait for all but this thread's last n groups of copies.
@@ -100,15 +80,15 @@ __device__ __forceinline__ void copies_wait(int n) {
     }
 }
 
-// A thread's place: its group (row) of the CTA and its rank there.
+// A thread's place: its group (row) of the CTA and its warp there.
 struct Place {
-    int tpr, group, groups, t, first_warp, warps;
-    __device__ __forceinline__ explicit Place(int tpr_) : tpr(tpr_) {
-        groups = blockDim.x / tpr;
-        group = threadIdx.x / tpr;
-        t = threadIdx.x - group * tpr;
-        warps = tpr >> 5;
-        first_warp = group * warps;
+    int group, groups, warps, warp, lane;
+    __device__ __forceinline__ explicit Place(int warps_) : warps(warps_) {
+        const int w = threadIdx.x >> 5;
+        groups = (blockDim.x >> 5) / warps;
+        group = w / warps;
+        warp = w - group * warps;
+        lane = threadIdx.x & 31;
     }
     // Sum over the group's threads (every thread gets it), in a fixed order.
     // red: a float per warp of the CTA, not the last call's; all threads of the
@@ -116,111 +96,176 @@ struct Place {
     __device__ __forceinline__ float sum(float v, float* red) const {
         v = warp_sum(v);
         if (warps > 1) {
-            if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-            asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(tpr) : "memory");
+            float* r = red + group * warps;
+            if (lane == 0) r[warp] = v;
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * warps) : "memory");
             v = 0.f;
-            for (int w = 0; w < warps; ++w) v += red[first_warp + w];
+            for (int w = 0; w < warps; ++w) v += r[w];
         }
         return v;
     }
 };
 
+// The largest of each of NC values over LANES neighbouring lanes (16 or 32),
+// all NC at once: as long as a lane holds several values it gives half of them
+// away for the other lane's share of the rest.  Value i ends in the lanes whose
+// number among the LANES, without its low SHIFT bits, is i.
+template <int NC, int LANES>
+struct BlockMax {
+    static constexpr int LOGV = NC <= 1 ? 0 : NC <= 2 ? 1 : NC <= 4 ? 2 : 3, V = 1 << LOGV;
+    static constexpr int SHIFT = (LANES == 32 ? 5 : 4) - LOGV;
+    static __device__ __forceinline__ uint32_t reduce(const uint32_t (&in)[NC], int lane) {
+        uint32_t m[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) m[i] = i < NC ? in[i] : 0u;
+        int n = V;
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) {
+            if (n > 1) {
+                n >>= 1;
+                const bool up = lane & o;
+#pragma unroll
+                for (int j = 0; j < V / 2; ++j) {
+                    if (j < n) {
+                        const uint32_t keep = up ? m[j + n] : m[j], give = up ? m[j] : m[j + n];
+                        m[j] = max(keep, __shfl_xor_sync(0xffffffffu, give, o));
+                    }
+                }
+            } else {
+                m[0] = max(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+            }
+        }
+        return m[0];
+    }
+};
+
+// gamma from shared memory where the launch gave it a place there (at the
+// ring's start): with the ring beside it, L1 holds no row's worth of it, and
+// reading it from L2 for every row doubled the traffic of wide rows.
+__device__ __forceinline__ const float* stage_gamma(const float* gamma, unsigned char* ring, int D, int gamma_bytes) {
+    if (!gamma || !gamma_bytes) return gamma;
+    for (int i = threadIdx.x; i < D / 4; i += blockDim.x)
+        reinterpret_cast<float4*>(ring)[i] = reinterpret_cast<const float4*>(gamma)[i];
+    __syncthreads();
+    return reinterpret_cast<const float*>(ring);
+}
+
 template <typename E, int NC, bool RESID>
-__global__ void __launch_bounds__(kCta, 1) rmsnorm_kernel(const RmsNorm p, int tpr, int stages) {
+__global__ void __launch_bounds__(kCta, 1) rmsnorm_kernel(const RmsNorm p, int warps, int stages, int gamma_bytes) {
     __shared__ float red[2][kCta / 32];
     extern __shared__ __align__(16) unsigned char ring[];
     pdl_enter();
-    const Place at(tpr);
-    const int nch = p.D / 8;
+    const Place at(warps);
+    using C = Chunk<E>;
+    const int nch = p.D / C::CE, c0 = at.warp * (NC * 32) + at.lane;
     const float inv_d = 1.0f / (float)p.D;
-    const uint32_t bytes = (uint32_t)(p.D * sizeof(E)), slot = bytes * (RESID ? 2 : 1);
-    const uint32_t mine = smem_u32(ring) + (uint32_t)(at.group * stages) * slot + (uint32_t)at.t * 8 * sizeof(E);
-    const uint32_t hop = (uint32_t)tpr * 8 * sizeof(E);   // from a thread's chunk to its next
+    constexpr uint32_t HOP = 32 * 16;   // bytes from a thread's chunk to its next
+    const uint32_t bytes = (uint32_t)p.D * sizeof(E), slot = bytes * (RESID ? 2 : 1);
+    const uint32_t mine = smem_u32(ring) + (uint32_t)gamma_bytes + (uint32_t)(at.group * stages) * slot + (uint32_t)c0 * 16;
     const long long step = (long long)gridDim.x * at.groups;
     long long row = (long long)blockIdx.x * at.groups + at.group;
-    auto fetch = [&](long long r, int s) {
-        if (r < p.rows) {
+    const char* nx = static_cast<const char*>(p.X) + row * p.ld_x * (long long)sizeof(E) + 16 * c0;
+    const char* nr = RESID ? static_cast<const char*>(p.R) + row * p.ld_r * (long long)sizeof(E) + 16 * c0 : nullptr;
+    long long ahead = row;   // the row that nx, nr point at
+    auto fetch = [&](uint32_t place) {
+        if (ahead < p.rows) {
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
-                const int c = at.t + i * tpr;
-                if (c < nch) {
-                    copy_chunk<E>(mine + s * slot + i * hop, p.X, r * p.ld_x + 8 * c);
-                    if constexpr (RESID) copy_chunk<E>(mine + s * slot + bytes + i * hop, p.R, r * p.ld_r + 8 * c);
+                if (c0 + 32 * i < nch) {
+                    copy_chunk(place + i * HOP, nx + i * HOP);
+                    if constexpr (RESID) copy_chunk(place + bytes + i * HOP, nr + i * HOP);
                 }
             }
         }
         copies_commit();
+        ahead += step;
+        nx += step * p.ld_x * (long long)sizeof(E);
+        if constexpr (RESID) nr += step * p.ld_r * (long long)sizeof(E);
     };
-    for (int s = 0; s < stages - 1; ++s) fetch(row + s * step, s);
-    int s = 0, last = stages - 1;   // the ring's place of this row and of the row stages - 1 on
+    for (int s = 0; s < stages; ++s) fetch(mine + s * slot);
+    const float* gamma = stage_gamma(p.gamma, ring, p.D, gamma_bytes);
+    uint32_t now = mine;   // place of this row, and of the row `stages` on as soon as this one is read
+    const uint32_t end = mine + stages * slot;
     for (int par = 0; row < p.rows; row += step, par ^= 1) {   // (one value of row per group)
-        fetch(row + (stages - 1) * step, last);
         copies_wait(stages - 1);
-        Chunk<E> x[NC];
+        C x[NC];
         float2 sq = f2(0.f);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            const int c = at.t + i * tpr;
-            if (c < nch) {
-                float2 v[4];
-                x[i].read(mine + s * slot + i * hop);
+            if (c0 + 32 * i < nch) {
+                float2 v[C::P];
+                x[i].read(now + i * HOP);
                 x[i].pairs(v);
                 if constexpr (RESID) {
                     // the stream is rounded to its type here: the statistics, the
                     // output and the gradient all see the values that are stored
-                    Chunk<E> r;
-                    float2 q[4];
-                    r.read(mine + s * slot + bytes + i * hop);
+                    C r;
+                    float2 q[C::P];
+                    r.read(now + bytes + i * HOP);
                     r.pairs(q);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = f2_add(v[e], q[e]);
+                    for (int e = 0; e < C::P; ++e) v[e] = f2_add(v[e], q[e]);
                     x[i].set(v);
                     x[i].pairs(v);
                 }
-                if (p.Sum) x[i].store(p.Sum, row * p.ld_sum + 8 * c);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sq = f2_fma(v[e], v[e], sq);
+                for (int e = 0; e < C::P; ++e) sq = f2_fma(v[e], v[e], sq);
             } else {
                 x[i].clear();
             }
         }
-        last = s;
-        s = s + 1 == stages ? 0 : s + 1;
+        fetch(now);
+        now = now + slot == end ? mine : now + slot;
+        if (p.Sum) {
+            char* o = static_cast<char*>(p.Sum) + row * p.ld_sum * (long long)sizeof(E) + 16 * c0;
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+                if (c0 + 32 * i < nch) x[i].store(o + i * HOP);
+        }
         const float rstd = inv_sqrt(fmaf(at.sum(sq.x + sq.y, red[par]), inv_d, p.eps));
-        if (p.rstd && at.t == 0) p.rstd[row] = rstd;
+        if (p.rstd && at.warp == 0 && at.lane == 0) p.rstd[row] = rstd;
+        if (!p.Y && !p.Yq) continue;
+        float2 y[NC][C::P];
+        uint32_t m[NC];
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            const int c = at.t + i * tpr;
-            const bool in = c < nch;
-            float2 y[4];
-            x[i].pairs(y);
+            const int c = c0 + 32 * i;
+            x[i].pairs(y[i]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = f2_mul(y[e], f2(rstd));
-            if (in && p.gamma) {
-                float2 g[4];
-                load_params(p.gamma + 8 * c, g);
+            for (int e = 0; e < C::P; ++e) y[i][e] = f2_mul(y[i][e], f2(rstd));
+            if (gamma && c < nch) {
+                float2 g[C::P];
+                load_params(gamma + C::CE * c0 + 32 * C::CE * i, g);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = f2_mul(y[e], g[e]);
+                for (int e = 0; e < C::P; ++e) y[i][e] = f2_mul(y[i][e], g[e]);
             }
-            if (in && p.Y) {
-                Chunk<E> o;
-                o.set(y);
-                o.store(p.Y, row * p.ld_y + 8 * c);
+            float mf = 0.f;
+#pragma unroll
+            for (int e = 0; e < C::P; ++e) mf = max_abs(mf, y[i][e]);
+            m[i] = c < nch ? abs_bits(mf) : 0u;
+        }
+        if (p.Y) {
+            char* o = static_cast<char*>(p.Y) + row * p.ld_y * (long long)sizeof(E) + 16 * c0;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                C k;
+                k.set(y[i]);
+                if (c0 + 32 * i < nch) k.store(o + i * HOP);
             }
-            if (p.Yq) {   // (whole warps: tpr is a multiple of 32)
-                float mf = 0.f;
+        }
+        if (p.Yq) {
+            using Max = BlockMax<NC, C::LANES>;
+            const uint32_t b = scale_byte(Max::reduce(m, at.lane));   // of the lanes' block `held` of NC
+            const float inv = scale_inverse(b);
+            const int held = (at.lane & (C::LANES - 1)) >> Max::SHIFT, half = at.lane & (32 - C::LANES);
+            const int block = (at.warp * (NC * 32) + 32 * held + half) / C::LANES;
+            if ((at.lane & ((1 << Max::SHIFT) - 1)) == 0 && held < NC && C::LANES * block < nch)
+                p.Ys[row * p.ld_ys + block] = (uint8_t)b;
+            char* o = static_cast<char*>(p.Yq) + row * p.ld_yq + C::CE * c0;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) mf = max_abs(mf, y[e]);
-                uint32_t m = in ? abs_bits(mf) : 0u;
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-                const uint32_t b = scale_byte(m);
-                const float2 inv = f2(scale_inverse(b));
-                if (in) {
-                    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.Yq) + row * p.ld_yq + 8 * c) =
-                        make_uint2(e4m3x4(f2_mul(y[0], inv), f2_mul(y[1], inv)), e4m3x4(f2_mul(y[2], inv), f2_mul(y[3], inv)));
-                    if ((threadIdx.x & 15) == 0) p.Ys[row * p.ld_ys + c / 16] = (uint8_t)b;
-                }
+            for (int i = 0; i < NC; ++i) {
+                const float2 k = f2(__shfl_sync(0xffffffffu, inv, half | (i << Max::SHIFT)));
+                if (c0 + 32 * i < nch) store_codes(o + 32 * C::CE * i, y[i], k);
             }
         }
     }
@@ -229,100 +274,102 @@ __global__ void __launch_bounds__(kCta, 1) rmsnorm_kernel(const RmsNorm p, int t
 // Gradient: the groups keep their columns' sums of dy * s * rstd in registers;
 // a CTA's groups add theirs in order and leave one partial row.
 template <typename E, int NC>
-__global__ void __launch_bounds__(kCta, 1) rmsnorm_bwd_kernel(const RmsNormGrad p, int tpr, int stages) {
+__global__ void __launch_bounds__(kCta, 1) rmsnorm_bwd_kernel(const RmsNormGrad p, int warps, int stages, int gamma_bytes) {
     __shared__ float red[2][kCta / 32];
     extern __shared__ __align__(16) unsigned char ring[];
     pdl_enter();
-    const Place at(tpr);
-    const int nch = p.D / 8;
-    const uint32_t bytes = (uint32_t)(p.D * sizeof(E)), slot = bytes * (p.dSum ? 3 : 2);
-    const uint32_t mine = smem_u32(ring) + (uint32_t)(at.group * stages) * slot + (uint32_t)at.t * 8 * sizeof(E);
-    const uint32_t hop = (uint32_t)tpr * 8 * sizeof(E);
+    const Place at(warps);
+    using C = Chunk<E>;
+    const int nch = p.D / C::CE, c0 = at.warp * (NC * 32) + at.lane;
     const float inv_d = 1.0f / (float)p.D;
-    float2 acc[NC][4];
-#pragma unroll
-    for (int i = 0; i < NC; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][e] = f2(0.f);
+    constexpr uint32_t HOP = 32 * 16;
+    const uint32_t bytes = (uint32_t)p.D * sizeof(E), slot = bytes * (p.dSum ? 3 : 2);
+    const uint32_t mine = smem_u32(ring) + (uint32_t)gamma_bytes + (uint32_t)(at.group * stages) * slot + (uint32_t)c0 * 16;
     const long long step = (long long)gridDim.x * at.groups;
     long long row = (long long)blockIdx.x * at.groups + at.group;
-    auto fetch = [&](long long r, int s) {
-        if (r < p.rows) {
+    auto place = [&](const void* base, long long ld) {
+        return static_cast<const char*>(base) + row * ld * (long long)sizeof(E) + 16 * c0;
+    };
+    const char* ns = place(p.S, p.ld_s);
+    const char* ny = place(p.dY, p.ld_dy);
+    const char* nd = p.dSum ? place(p.dSum, p.ld_dsum) : nullptr;
+    long long ahead = row;
+    auto fetch = [&](uint32_t to) {
+        if (ahead < p.rows) {
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
-                const int c = at.t + i * tpr;
-                if (c < nch) {
-                    const uint32_t d = mine + s * slot + i * hop;
-                    copy_chunk<E>(d, p.S, r * p.ld_s + 8 * c);
-                    copy_chunk<E>(d + bytes, p.dY, r * p.ld_dy + 8 * c);
-                    if (p.dSum) copy_chunk<E>(d + 2 * bytes, p.dSum, r * p.ld_dsum + 8 * c);
+                if (c0 + 32 * i < nch) {
+                    copy_chunk(to + i * HOP, ns + i * HOP);
+                    copy_chunk(to + bytes + i * HOP, ny + i * HOP);
+                    if (nd) copy_chunk(to + 2 * bytes + i * HOP, nd + i * HOP);
                 }
             }
         }
         copies_commit();
+        ahead += step;
+        ns += step * p.ld_s * (long long)sizeof(E);
+        ny += step * p.ld_dy * (long long)sizeof(E);
+        if (nd) nd += step * p.ld_dsum * (long long)sizeof(E);
     };
-    for (int s = 0; s < stages - 1; ++s) fetch(row + s * step, s);
-    int s = 0, last = stages - 1;
+    float2 acc[NC][C::P];
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int e = 0; e < C::P; ++e) acc[i][e] = f2(0.f);
+    for (int s = 0; s < stages - 1; ++s) fetch(mine + s * slot);
+    const float* gamma = stage_gamma(p.gamma, ring, p.D, gamma_bytes);
+    uint32_t now = mine, last = mine + (stages - 1) * slot;   // places of this row and of the row stages - 1 on
+    const uint32_t end = mine + stages * slot;
     float rstd = row < p.rows ? __ldcg(p.rstd + row) : 0.f;
     for (int par = 0; row < p.rows; row += step, par ^= 1) {
-        fetch(row + (stages - 1) * step, last);
+        fetch(last);
         const float next_rstd = row + step < p.rows ? __ldcg(p.rstd + row + step) : 0.f;
         copies_wait(stages - 1);
-        float2 dots = f2(0.f);
+        C cs[NC];
+        float2 a[NC][C::P], dots = f2(0.f);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            const int c = at.t + i * tpr;
-            if (c < nch) {
-                Chunk<E> cs, cy;
-                float2 sv[4], dy[4];
-                cs.read(mine + s * slot + i * hop);
-                cy.read(mine + s * slot + i * hop + bytes);
-                cs.pairs(sv);
-                cy.pairs(dy);
+            if (c0 + 32 * i < nch) {
+                C cy;
+                float2 sv[C::P];
+                cs[i].read(now + i * HOP);
+                cy.read(now + i * HOP + bytes);
+                cs[i].pairs(sv);
+                cy.pairs(a[i]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][e] = f2_fma(f2_mul(dy[e], f2(rstd)), sv[e], acc[i][e]);
-                if (p.gamma) {
-                    float2 g[4];
-                    load_params(p.gamma + 8 * c, g);
+                for (int e = 0; e < C::P; ++e) acc[i][e] = f2_fma(f2_mul(a[i][e], f2(rstd)), sv[e], acc[i][e]);
+                if (gamma) {
+                    float2 g[C::P];
+                    load_params(gamma + C::CE * c0 + 32 * C::CE * i, g);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) dy[e] = f2_mul(dy[e], g[e]);
+                    for (int e = 0; e < C::P; ++e) a[i][e] = f2_mul(a[i][e], g[e]);
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) dots = f2_fma(dy[e], sv[e], dots);
+                for (int e = 0; e < C::P; ++e) dots = f2_fma(a[i][e], sv[e], dots);
             }
         }
         const float dot = at.sum(dots.x + dots.y, red[par]);
         const float2 k = f2(-rstd * rstd * (dot * inv_d));
+        char* o = static_cast<char*>(p.dX) + row * p.ld_dx * (long long)sizeof(E) + 16 * c0;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            const int c = at.t + i * tpr;
-            if (c < nch) {
-                Chunk<E> cs, cy;
-                float2 sv[4], dy[4];
-                cs.read(mine + s * slot + i * hop);
-                cy.read(mine + s * slot + i * hop + bytes);
-                cs.pairs(sv);
-                cy.pairs(dy);
-                if (p.gamma) {
-                    float2 g[4];
-                    load_params(p.gamma + 8 * c, g);
+            if (c0 + 32 * i < nch) {
+                float2 sv[C::P];
+                cs[i].pairs(sv);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) dy[e] = f2_mul(dy[e], g[e]);
+                for (int e = 0; e < C::P; ++e) a[i][e] = f2_mul(f2_fma(sv[e], k, a[i][e]), f2(rstd));
+                if (nd) {
+                    cs[i].read(now + i * HOP + 2 * bytes);
+                    cs[i].pairs(sv);
+#pragma unroll
+                    for (int e = 0; e < C::P; ++e) a[i][e] = f2_add(a[i][e], sv[e]);
                 }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) dy[e] = f2_mul(f2_fma(sv[e], k, dy[e]), f2(rstd));
-                if (p.dSum) {
-                    cs.read(mine + s * slot + i * hop + 2 * bytes);
-                    cs.pairs(sv);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) dy[e] = f2_add(dy[e], sv[e]);
-                }
-                cs.set(dy);
-                cs.store(p.dX, row * p.ld_dx + 8 * c);
+                cs[i].set(a[i]);
+                cs[i].store(o + i * HOP);
             }
         }
-        last = s;
-        s = s + 1 == stages ? 0 : s + 1;
+        last = now;
+        now = now + slot == end ? mine : now + slot;
         rstd = next_rstd;
     }
     if (!p.part) return;
@@ -334,18 +381,18 @@ __global__ void __launch_bounds__(kCta, 1) rmsnorm_bwd_kernel(const RmsNormGrad 
         if (at.group == k) {
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
-                const int c = at.t + i * tpr;
+                const int c = c0 + 32 * i;
                 if (c < nch) {
-                    float2* a = reinterpret_cast<float2*>(acc_s + 8 * c);
+                    float2* s = reinterpret_cast<float2*>(acc_s + C::CE * c);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (k) acc[i][e] = f2_add(acc[i][e], a[e]);
-                        if (k < at.groups - 1) a[e] = acc[i][e];
+                    for (int e = 0; e < C::P; ++e) {
+                        if (k) acc[i][e] = f2_add(acc[i][e], s[e]);
+                        if (k < at.groups - 1) s[e] = acc[i][e];
                     }
                     if (k == at.groups - 1) {
-                        Chunk<float> o;
-                        o.set(acc[i]);
-                        o.store(p.part, (long long)blockIdx.x * p.D + 8 * c);
+                        float2* out = reinterpret_cast<float2*>(p.part + (long long)blockIdx.x * p.D + C::CE * c);
+#pragma unroll
+                        for (int e = 0; e < C::P; ++e) out[e] = acc[i][e];
                     }
                 }
             }
@@ -376,47 +423,59 @@ __global__ void __launch_bounds__(1024) colsum_parts_kernel(const float* part, f
     if (lane == 0 && blockIdx.x * 32 + warp < D) out[blockIdx.x * 32 + warp] = v;
 }
 
-// Launch shape for rows of D whose `row_bytes` (all inputs) go through the ring.
+// Launch shape for rows of D elements of esz bytes, `inputs` of them through
+// the ring.
 struct Shape {
-    int nc, tpr, groups, threads, stages, grid;
+    int nc, warps, groups, threads, stages, grid, gamma_bytes;
     size_t smem;
-    Shape(long long rows, int D, size_t row_bytes) {
-        const int nch = D / 8;
-        // Warps a row: as few as hold it in six chunks a thread (what a row costs
-        // besides, its sum and its waits, is then shared by 48 elements a thread),
-        // but all of them where the SMs have a row each.
-        const int most = (nch + 31) / 32;
-        int w = rows <= kSms ? most : (most + 5) / 6;
-        w = std::min(w, kCta / 32);
-        tpr = 32 * w;
-        nc = (nch + tpr - 1) / tpr;
-        groups = kCta / tpr;
-        if (tpr > 32) groups = std::min(groups, 15);   // (named barriers)
+    Shape(long long rows, int D, int esz, int inputs, bool gamma, int max_nc) {
+        const int most = (D * esz / 16 + 31) / 32;
+        const size_t row_bytes = (size_t)D * esz * inputs;
+        // Warps a row: as few as hold it in max_nc chunks a thread (what a row
+        // costs besides, its sum and its waits, is shared by those), but as many as
+        // there are chunks for where the SMs have a row each.
+        warps = std::min(rows <= kSms ? most : (most + max_nc - 1) / max_nc, kCta / 32);
+        nc = (most + warps - 1) / warps;
+        groups = kCta / 32 / warps;
+        if (warps > 1) groups = std::min(groups, 15);   // (named barriers)
         groups = (int)std::min<long long>(groups, (rows + kSms - 1) / kSms);
-        groups = (int)std::min<size_t>(groups, kRing / row_bytes);
-        stages = (int)std::min<size_t>(4, kRing / (row_bytes * groups));
-        threads = groups * tpr;
-        smem = row_bytes * groups * stages;
+        // two rows a group in the ring, one at least
+        const auto fit = [&](size_t room) { return (int)std::max<size_t>(1, std::min<size_t>(groups, room / (2 * row_bytes))); };
+        const int with = 4 * D + row_bytes <= kRing ? fit(kRing - 4 * D) : 0, without = fit(kRing);
+        // gamma in shared memory where several rows use it and no group gives way
+        gamma_bytes = gamma && rows > 2 * kSms && with == without ? 4 * D : 0;
+        groups = without;
+        stages = (int)std::min<size_t>(4, (kRing - gamma_bytes) / (row_bytes * groups));
+        threads = groups * warps * 32;
+        smem = gamma_bytes + row_bytes * groups * stages;
         grid = (int)std::min<long long>((rows + groups - 1) / groups, kSms);
     }
 };
+
+// Chunks a thread at most (what the registers hold without spilling).
+template <typename E>
+constexpr int kFwdChunks = sizeof(E) == 2 ? 6 : 8;
+template <typename E>
+constexpr int kBwdChunks = sizeof(E) == 2 ? 4 : 8;
 
 template <typename E, int NC, bool RESID>
 cudaError_t fwd(const RmsNorm& p, const Shape& sh, cudaStream_t s) {
     static SmemGrant grant;
     if (cudaError_t e = grant.ask(rmsnorm_kernel<E, NC, RESID>, kRing)) return e;
-    return launch_pdl(rmsnorm_kernel<E, NC, RESID>, dim3(sh.grid), dim3(sh.threads), sh.smem, s, p, sh.tpr, sh.stages);
+    return launch_pdl(rmsnorm_kernel<E, NC, RESID>, dim3(sh.grid), dim3(sh.threads), sh.smem, s, p, sh.warps, sh.stages,
+                      sh.gamma_bytes);
 }
 template <typename E, bool RESID>
 cudaError_t fwd_e(const RmsNorm& p, cudaStream_t s) {
-    const Shape sh(p.rows, p.D, sizeof(E) * p.D * (RESID ? 2 : 1));
+    const Shape sh(p.rows, p.D, sizeof(E), RESID ? 2 : 1, p.gamma != nullptr, kFwdChunks<E>);
     switch (sh.nc) {
         case 1: return fwd<E, 1, RESID>(p, sh, s);
         case 2: return fwd<E, 2, RESID>(p, sh, s);
         case 3: return fwd<E, 3, RESID>(p, sh, s);
         case 4: return fwd<E, 4, RESID>(p, sh, s);
-        case 5: return fwd<E, 5, RESID>(p, sh, s);
-        default: return fwd<E, 6, RESID>(p, sh, s);
+        case 5:
+        case 6: return fwd<E, 6, RESID>(p, sh, s);
+        default: return fwd<E, kFwdChunks<E>, RESID>(p, sh, s);
     }
 }
 
@@ -424,18 +483,20 @@ template <typename E, int NC>
 cudaError_t bwd(const RmsNormGrad& p, const Shape& sh, cudaStream_t s) {
     static SmemGrant grant;
     if (cudaError_t e = grant.ask(rmsnorm_bwd_kernel<E, NC>, kRing)) return e;
-    return launch_pdl(rmsnorm_bwd_kernel<E, NC>, dim3(sh.grid), dim3(sh.threads), sh.smem, s, p, sh.tpr, sh.stages);
+    return launch_pdl(rmsnorm_bwd_kernel<E, NC>, dim3(sh.grid), dim3(sh.threads), sh.smem, s, p, sh.warps, sh.stages,
+                      sh.gamma_bytes);
 }
 
 template <typename E>
-cudaError_t bwd_e(const RmsNormGrad& p, const Shape& sh, cudaStream_t s) {
+cudaError_t bwd_e(const RmsNormGrad& p, int* parts, cudaStream_t s) {
+    const Shape sh(p.rows, p.D, sizeof(E), p.dSum ? 3 : 2, p.gamma != nullptr, kBwdChunks<E>);
+    *parts = sh.grid;
     switch (sh.nc) {
         case 1: return bwd<E, 1>(p, sh, s);
         case 2: return bwd<E, 2>(p, sh, s);
         case 3: return bwd<E, 3>(p, sh, s);
         case 4: return bwd<E, 4>(p, sh, s);
-        case 5: return bwd<E, 5>(p, sh, s);
-        default: return bwd<E, 6>(p, sh, s);
+        default: return bwd<E, kBwdChunks<E>>(p, sh, s);
     }
 }
 
@@ -450,10 +511,10 @@ cudaError_t launch_rmsnorm(int dtype, const RmsNorm& p, cudaStream_t s) {
 int rmsnorm_bwd_parts(long long rows) { return (int)std::min<long long>(rows, kSms); }
 
 cudaError_t launch_rmsnorm_bwd(int dtype, const RmsNormGrad& p, float* dgamma, cudaStream_t s) {
-    const Shape sh(p.rows, p.D, (dtype == RM_BF16 ? 2 : 4) * (size_t)p.D * (p.dSum ? 3 : 2));
-    const cudaError_t e = dtype == RM_BF16 ? bwd_e<__nv_bfloat16>(p, sh, s) : bwd_e<float>(p, sh, s);
+    int parts;
+    const cudaError_t e = dtype == RM_BF16 ? bwd_e<__nv_bfloat16>(p, &parts, s) : bwd_e<float>(p, &parts, s);
     if (e != cudaSuccess || !dgamma) return e;
-    return launch_pdl(colsum_parts_kernel, dim3((p.D + 31) / 32), dim3(1024), 0, s, (const float*)p.part, dgamma, sh.grid,
+    return launch_pdl(colsum_parts_kernel, dim3((p.D + 31) / 32), dim3(1024), 0, s, (const float*)p.part, dgamma, parts,
                       p.D);
 }
 
