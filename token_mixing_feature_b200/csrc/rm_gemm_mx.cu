@@ -105,9 +105,9 @@ __device__ __forceinline__ void finish(float (&v)[kFrag], const MxParams& p, uin
         }
     }
     switch (p.act) {
-        case RM_ACT_GELU_TANH: activate<RM_ACT_GELU_TANH, OUT == RM_F32>(v); break;
-        case RM_ACT_GELU_ERF: activate<RM_ACT_GELU_ERF, OUT == RM_F32>(v); break;
-        case RM_ACT_RELU: activate<RM_ACT_RELU, OUT == RM_F32>(v); break;
+        case RM_ACT_GELU_TANH: activate<RM_ACT_GELU_TANH, OUT != RM_BF16>(v); break;
+        case RM_ACT_GELU_ERF: activate<RM_ACT_GELU_ERF, OUT != RM_BF16>(v); break;
+        case RM_ACT_RELU: activate<RM_ACT_RELU, OUT != RM_BF16>(v); break;
         default: break;
     }
     if (OUT != RM_E4M3 && p.resid) {
