@@ -35,8 +35,7 @@ constexpr int kSlots = 4;          // chunks (512 of K) of scale atoms in shared
 constexpr int kTSlots = 2;         // ... and in tensor memory
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = (4 + kEpiWarps) * 32;
-constexpr int kOutBoxes = 4;       // staging of an epilogue warp's output: boxes of 16 rows x 128 bytes
-constexpr int kOutBytes = kOutBoxes * 2048;
+constexpr int kOutBytes = 8192;    // staging of an epilogue warp's output
 
 struct Cfg {
     static constexpr int B_ROWS = BN / 2;                  // W rows a CTA loads
@@ -68,14 +67,84 @@ __device__ __forceinline__ Tile decode(uint32_t idx, uint32_t mblk, uint32_t nbl
     return Tile{(int)g, (int)(idx - col * mblk) * TM, (int)(col - g * nblk) * BN};
 }
 
-// An epilogue warp's share of a tile is 32 rows x 128 columns, taken as two
-// halves of 16 rows: 64 values a thread, so that a row's 128 columns (one
-// quantisation block) lie in the four lanes of a quad.  Fragment of a half:
-// v[4 i + 2 h + j] is row lane / 4 + 8 h, column 8 i + 2 (lane % 4) + j.
+template <int OUT, int NV>
+__device__ __forceinline__ void activate_all(float (&v)[NV], int act) {
+    switch (act) {
+        case RM_ACT_GELU_TANH: activate<RM_ACT_GELU_TANH, OUT != RM_BF16>(v); break;
+        case RM_ACT_GELU_ERF: activate<RM_ACT_GELU_ERF, OUT != RM_BF16>(v); break;
+        case RM_ACT_RELU: activate<RM_ACT_RELU, OUT != RM_BF16>(v); break;
+        default: break;
+    }
+}
+
+// ---- bf16 and fp32 results: an epilogue warp takes its 32 rows x 128 columns
+// in chunks of 64 columns, a row a thread.
+constexpr int kChunk = 64;
+
+__device__ __forceinline__ void load_rows(uint32_t taddr, float (&v)[kChunk]) {
+#pragma unroll
+    for (int q = 0; q < kChunk / 16; ++q) {
+        float w[16];
+        tmem_ld16(taddr + 16 * q, w);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[16 * q + e] = w[e];
+    }
+    tmem_ld_wait();
+}
+
+// bias (from shared memory), activation and residual of columns n .. n + 63 of
+// row m (live: it exists), in place.
+template <int OUT>
+__device__ __forceinline__ void finish_row(float (&v)[kChunk], const MxParams& p, uint32_t bias, int g, int m, int n,
+                                           bool live) {
+    if (p.bias) {
+#pragma unroll
+        for (int q = 0; q < kChunk / 4; ++q) {
+            const float4 x = lds_f32x4(bias + 16 * q);
+            const float2 lo = f2_add(make_float2(v[4 * q], v[4 * q + 1]), make_float2(x.x, x.y));
+            const float2 hi = f2_add(make_float2(v[4 * q + 2], v[4 * q + 3]), make_float2(x.z, x.w));
+            v[4 * q] = lo.x, v[4 * q + 1] = lo.y, v[4 * q + 2] = hi.x, v[4 * q + 3] = hi.y;
+        }
+    }
+    activate_all<OUT>(v, p.act);
+    if (p.resid && live) {
+        constexpr int E = OUT == RM_F32 ? 4 : 8;   // elements of a 16-byte vector
+        const char* r = static_cast<const char*>(p.resid) + (g * p.r_gs + m * p.r_ld + n) * (16 / E);
+#pragma unroll
+        for (int q = 0; q < kChunk / E; ++q) {
+            if (n + E * q >= p.N) break;   // (N is a multiple of 16)
+            float2 f[E / 2];
+            unpack_pairs(reinterpret_cast<const uint4*>(r)[q], f);
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) v[E * q + 2 * e] += f[e].x, v[E * q + 2 * e + 1] += f[e].y;
+        }
+    }
+}
+
+// The chunk into boxes of 32 rows x 128 bytes (two of fp32, one of bf16), in
+// the 128-byte swizzle of the bulk stores.
+template <int OUT>
+__device__ __forceinline__ void stage_rows(const float (&v)[kChunk], uint32_t buf, int lane) {
+    const uint32_t row = buf + 128u * (uint32_t)lane, sw = (uint32_t)(lane & 7);
+#pragma unroll
+    for (int j = 0; j < (OUT == RM_F32 ? 16 : 8); ++j) {
+        const uint32_t at = row + 4096u * (uint32_t)(j / 8) + (((uint32_t)(j % 8) ^ sw) << 4);
+        if constexpr (OUT == RM_F32)
+            sts128(at, make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),
+                                  __float_as_uint(v[4 * j + 3])));
+        else
+            sts128(at, make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                                  pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7])));
+    }
+}
+
+// ---- e4m3 results: two halves of 16 rows x 128 columns, 64 values a thread,
+// so that a row's 128 columns (one quantisation block) lie in the four lanes of
+// a quad.  Fragment of a half: v[4 i + 2 h + j] is row lane / 4 + 8 h, column
+// 8 i + 2 (lane % 4) + j.
 constexpr int kFrag = 64;
 
-// Four of the 32-column pieces of 16 accumulator rows; piece `skip` (if any)
-// stays as it was.
+// A 32-column piece of 16 accumulator rows.
 __device__ __forceinline__ void load_piece(uint32_t taddr, float* v) {
     uint32_t r[16];
     asm volatile(
@@ -88,11 +157,8 @@ __device__ __forceinline__ void load_piece(uint32_t taddr, float* v) {
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// bias (128 floats in shared memory), activation and residual, in place.
-// row0: the half's first row; n: the tile's first column of this warp.
-template <int OUT>
-__device__ __forceinline__ void finish(float (&v)[kFrag], const MxParams& p, uint32_t bias, int g, int row0, int n,
-                                       int lane) {
+// bias (128 floats in shared memory) and activation, in place.
+__device__ __forceinline__ void finish_quads(float (&v)[kFrag], const MxParams& p, uint32_t bias, int lane) {
     if (p.bias) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -104,45 +170,24 @@ __device__ __forceinline__ void finish(float (&v)[kFrag], const MxParams& p, uin
             }
         }
     }
-    switch (p.act) {
-        case RM_ACT_GELU_TANH: activate<RM_ACT_GELU_TANH, OUT != RM_BF16>(v); break;
-        case RM_ACT_GELU_ERF: activate<RM_ACT_GELU_ERF, OUT != RM_BF16>(v); break;
-        case RM_ACT_RELU: activate<RM_ACT_RELU, OUT != RM_BF16>(v); break;
-        default: break;
-    }
-    if (OUT != RM_E4M3 && p.resid) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int m = row0 + (lane >> 2) + 8 * h;
-            if (m >= p.M) continue;
-            const long long at = g * p.r_gs + m * p.r_ld + n + 2 * (lane & 3);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                if (n + 8 * i >= p.N) break;   // (N is a multiple of 16)
-                float2 r;
-                if constexpr (OUT == RM_F32) {
-                    r = *reinterpret_cast<const float2*>(static_cast<const float*>(p.resid) + at + 8 * i);
-                } else {
-                    const uint32_t u = *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.resid) + at + 8 * i);
-                    r = make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-                }
-                v[4 * i + 2 * h] += r.x, v[4 * i + 2 * h + 1] += r.y;
-            }
-        }
-    }
+    activate_all<RM_E4M3>(v, p.act);
 }
 
-// e4m3 output: the scale of each of the thread's two rows (its quad's largest
-// magnitude over the columns below N), the byte to memory; inv: its inverse.
+// The scale of each of the thread's two rows (its quad's largest magnitude over
+// the columns below N), the byte to memory; inv: its inverse.
 __device__ __forceinline__ void row_scales(const float (&v)[kFrag], float (&inv)[2], const MxParams& p, int g, int row0,
                                            int n, int lane) {
+    float mf[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        if (n + 8 * i < p.N) {
+            mf[0] = max_abs(mf[0], make_float2(v[4 * i], v[4 * i + 1]));
+            mf[1] = max_abs(mf[1], make_float2(v[4 * i + 2], v[4 * i + 3]));
+        }
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        float mf = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (n + 8 * i < p.N) mf = max_abs(mf, make_float2(v[4 * i + 2 * h], v[4 * i + 2 * h + 1]));
-        uint32_t mx = abs_bits(mf);
+        uint32_t mx = abs_bits(mf[h]);
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         const uint32_t b = scale_byte(mx);
@@ -152,36 +197,24 @@ __device__ __forceinline__ void row_scales(const float (&v)[kFrag], float (&inv)
     }
 }
 
-// One box (16 rows x 128 bytes, in the 128-byte swizzle of the bulk stores) of
-// the half: all 128 columns of e4m3, 64 of bf16, 32 of fp32.
-template <int OUT>
-__device__ __forceinline__ void stage_box(const float* v, uint32_t buf, const float (&inv)[2], int lane) {
+// The half's codes into a box of 16 rows x 128 bytes, swizzled.
+__device__ __forceinline__ void stage_quads(const float (&v)[kFrag], uint32_t buf, const float (&inv)[2], int lane) {
     const int q = lane & 3, r7 = lane >> 2;   // row lane / 4 + 8 h: the swizzle's row is r7 for both h
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const uint32_t row = buf + 128u * (uint32_t)(r7 + 8 * h);
-        if constexpr (OUT == RM_BF16) {
+        const float2 k = f2(inv[h]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                sts32(row + ((i ^ r7) << 4) + 4 * q, pack_bf16x2(v[4 * i + 2 * h], v[4 * i + 2 * h + 1]));
-        } else if constexpr (OUT == RM_F32) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                sts64(row + (((2 * i + q / 2) ^ r7) << 4) + 8 * (q & 1),
-                      make_uint2(__float_as_uint(v[4 * i + 2 * h]), __float_as_uint(v[4 * i + 2 * h + 1])));
-        } else {
-            const float2 k = f2(inv[h]);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float2 y = f2_mul(make_float2(v[4 * i + 2 * h], v[4 * i + 2 * h + 1]), k);
-                sts16(row + (((i / 2) ^ r7) << 4) + 8 * (i & 1) + 2 * q,
-                      __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3));
-            }
+        for (int i = 0; i < 16; ++i) {
+            const float2 y = f2_mul(make_float2(v[4 * i + 2 * h], v[4 * i + 2 * h + 1]), k);
+            sts16(row + (((i / 2) ^ r7) << 4) + 8 * (i & 1) + 2 * q, __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3));
         }
     }
 }
 
-template <int OUT>
+// PLAIN: no bias, activation or residual (each of their branches moves the 64
+// values of a thread between registers, untaken or not).
+template <int OUT, bool PLAIN>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_mx_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
                    const __grid_constant__ CUtensorMap tmO, const MxParams p) {
@@ -383,16 +416,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tempty_l = mapa_shared(tempty_bar, 0);
         const uint32_t stage = out0 + (uint32_t)(warp - 4) * kOutBytes;
         const uint32_t bias_s = out0 + kEpiWarps * kOutBytes + (uint32_t)(warp - 4) * 512u;
-        constexpr int ESZ = OUT == RM_F32 ? 4 : OUT == RM_BF16 ? 2 : 1;
-        constexpr int BOXES = ESZ;   // boxes of 16 rows x 128 bytes of a half; kOutBytes holds kOutBoxes, taking turns
-        int box = 0;
+        int buf = 0;   // staging buffer of the next store
         int it = 0;
         for (uint32_t idx = unit; idx < total; idx += nunits, ++it) {
             const int acc = it & 1;
             const Tile t = decode(idx, mblk, nblk);
             const int col0 = 128 * half;   // this group's 128 columns
             const int row0 = t.m0 + (int)rank * BM + quarter * 32, n = t.n0 + col0;
-            if (p.bias) {   // fetched while the tile's products run
+            if (!PLAIN && p.bias) {   // fetched while the tile's products run
                 float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (n + 4 * lane < p.N) x = *reinterpret_cast<const float4*>(p.bias + (long long)t.g * p.N + n + 4 * lane);
                 __syncwarp();
@@ -403,49 +434,76 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!warp_wait(tfull0 + 8 * acc, (uint32_t)(it >> 1) & 1u, wc, SITE_MX_EPILOGUE)) break;
             tc_fence_after();
             const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * C::ACC1 + col0);
-            // 32-column piece of this warp's share that the next tile's accumulator
-            // overlaps (its last of the first accumulator, its first of the second)
-            const int shared = acc == 0 ? (half == 1 ? 3 : -1) : (half == 0 ? 0 : -1);   // (none: -1)
-            float keep[16];
+            const auto release = [&] {   // the columns that the next tile's accumulator overlaps have been read
+                tc_fence_before();
+                if (leader) mbar_arrive(tempty_bar);
+                else mbar_arrive_cluster_relaxed(tempty_l);
+            };
+            const auto store = [&](uint32_t src, int c, int r) {
+                tma_store_3d(&tmO, src, c, p.o_g_inner ? t.g : r, p.o_g_inner ? r : t.g);
+            };
+            if constexpr (OUT != RM_E4M3) {
+                constexpr int ESZ = OUT == RM_F32 ? 4 : 2, BOXES = ESZ / 2, BUFS = 2 / BOXES;
+                // the overlap (the last 24 columns of the first accumulator, the first 24
+                // of the second) is in the chunk that is read first
+                const int first = acc == 0 && half == 1 ? 1 : 0;
 #pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t th = ta + ((uint32_t)(16 * h) << 16);
-                float v[kFrag];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (h == 0 || shared != j) load_piece(th + 32 * j, v + 16 * j);
-                if (h == 0 && shared >= 0) load_piece(ta + (16u << 16) + 32u * (uint32_t)shared, keep);
-                tmem_ld_wait();
-                if (h == 1) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        if (shared == 0) v[j] = keep[j];
-                        if (shared == 3) v[48 + j] = keep[j];
-                    }
-                }
-                if (h == 0) {   // the overlap may be written again
-                    tc_fence_before();
-                    if (leader) mbar_arrive(tempty_bar);
-                    else mbar_arrive_cluster_relaxed(tempty_l);
-                }
-                const int r0 = row0 + 16 * h;
-                if (r0 >= p.M || n >= p.N) continue;   // (one value per warp)
-                finish<OUT>(v, p, bias_s, t.g, r0, n, lane);
-                float inv[2] = {0.f, 0.f};
-                if constexpr (OUT == RM_E4M3) row_scales(v, inv, p, t.g, r0, n, lane);
-#pragma unroll
-                for (int b = 0; b < BOXES; ++b) {
-                    const int c = n + b * (128 / ESZ);
-                    if (c >= p.N) break;
-                    const uint32_t sb = stage + 2048u * (uint32_t)box;
-                    box = box + 1 == kOutBoxes ? 0 : box + 1;
-                    if (lane == 0) bulk_wait_read<kOutBoxes - 1>();   // the box's last store has read it
+                for (int k = 0; k < 2; ++k) {
+                    const int c = kChunk * (k ^ first);
+                    float v[kChunk];
+                    load_rows(ta + c, v);
+                    if (k == 0) release();
+                    if (row0 >= p.M || n + c >= p.N) continue;   // (one value per warp)
+                    if constexpr (!PLAIN) finish_row<OUT>(v, p, bias_s + 4 * c, t.g, row0 + lane, n + c, row0 + lane < p.M);
+                    const uint32_t sb = stage + 4096u * BOXES * (uint32_t)buf;
+                    buf = buf + 1 == BUFS ? 0 : buf + 1;
+                    if (lane == 0) bulk_wait_read<BUFS - 1>();   // the buffer's last store has read it
                     __syncwarp();
-                    stage_box<OUT>(v + b * (kFrag / BOXES), sb, inv, lane);
+                    stage_rows<OUT>(v, sb, lane);
                     fence_proxy_async_shared();
                     __syncwarp();
                     if (lane == 0) {
-                        tma_store_3d(&tmO, sb, c, p.o_g_inner ? t.g : r0, p.o_g_inner ? r0 : t.g);
+#pragma unroll
+                        for (int b = 0; b < BOXES; ++b)
+                            if (n + c + 32 * b < p.N) store(sb + 4096u * b, n + c + 32 * b, row0);
+                        bulk_commit_group();
+                    }
+                }
+            } else {
+                // 32-column piece with the overlap, of both halves read before anything else
+                const int shared = acc == 0 ? (half == 1 ? 3 : -1) : (half == 0 ? 0 : -1);   // (none: -1)
+                float keep[16];
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    float v[kFrag];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (h == 0 || shared != j) load_piece(ta + ((uint32_t)(16 * h) << 16) + 32 * j, v + 16 * j);
+                    if (h == 0 && shared >= 0) load_piece(ta + (16u << 16) + 32u * (uint32_t)shared, keep);
+                    tmem_ld_wait();
+                    if (h == 0) {
+                        release();
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            if (shared == 0) v[j] = keep[j];
+                            if (shared == 3) v[48 + j] = keep[j];
+                        }
+                    }
+                    const int r0 = row0 + 16 * h;
+                    if (r0 >= p.M || n >= p.N) continue;   // (one value per warp)
+                    if constexpr (!PLAIN) finish_quads(v, p, bias_s, lane);
+                    float inv[2];
+                    row_scales(v, inv, p, t.g, r0, n, lane);
+                    const uint32_t sb = stage + 2048u * (uint32_t)buf;
+                    buf = buf + 1 & 3;
+                    if (lane == 0) bulk_wait_read<3>();
+                    __syncwarp();
+                    stage_quads(v, sb, inv, lane);
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        store(sb, n, r0);
                         bulk_commit_group();
                     }
                 }
@@ -464,21 +522,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int OUT>
+template <int OUT, bool PLAIN>
 cudaError_t launch_tile(const rm_matmul_fp8_args& a, MxParams& p, int num_sms, cudaStream_t s) {
     using C = Cfg;
     static SmemGrant grant;
-    if (cudaError_t e = grant.ask(gemm_mx_kernel<OUT>, C::SMEM_BYTES)) return e;
+    if (cudaError_t e = grant.ask(gemm_mx_kernel<OUT, PLAIN>, C::SMEM_BYTES)) return e;
     CUtensorMap ma, mw, mo;
+    const int osz = OUT == RM_F32 ? 4 : OUT == RM_BF16 ? 2 : 1, orows = OUT == RM_E4M3 ? 16 : 32;
     if (!matrix_map(&ma, a.A, a.K, a.M, a.G, a.a_ld, a.a_gstride, 1, BM, &p.a_g_inner, &p.a_gmul) ||
         !matrix_map(&mw, a.W, a.K, a.N, a.G, a.w_ld, a.w_gstride, 1, C::B_ROWS, &p.w_g_inner, &p.w_gmul) ||
-        !matrix_map(&mo, a.out, a.N, a.M, a.G, a.o_ld, a.o_gstride, OUT == RM_F32 ? 4 : OUT == RM_BF16 ? 2 : 1, 16,
-                    &p.o_g_inner, nullptr))
+        !matrix_map(&mo, a.out, a.N, a.M, a.G, a.o_ld, a.o_gstride, osz, orows, &p.o_g_inner, nullptr))
         return cudaErrorInvalidValue;
-    const long long tiles =
-        (long long)a.G * ((a.M + TM - 1) / TM) * ((a.N + BN - 1) / BN);
+    const long long tiles = (long long)a.G * ((a.M + TM - 1) / TM) * ((a.N + BN - 1) / BN);
     const int units = (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
-    return launch_cluster(gemm_mx_kernel<OUT>, dim3(units * 2), kThreads, C::SMEM_BYTES, 2, s, ma, mw, mo, p);
+    return launch_cluster(gemm_mx_kernel<OUT, PLAIN>, dim3(units * 2), kThreads, C::SMEM_BYTES, 2, s, ma, mw, mo, p);
+}
+template <int OUT>
+cudaError_t launch_out(const rm_matmul_fp8_args& a, MxParams& p, int num_sms, cudaStream_t s) {
+    const bool plain = !a.bias && !a.resid && a.act == RM_ACT_NONE;
+    return plain ? launch_tile<OUT, true>(a, p, num_sms, s) : launch_tile<OUT, false>(a, p, num_sms, s);
 }
 
 }  // namespace
@@ -512,9 +574,9 @@ cudaError_t launch_gemm_mx(const rm_matmul_fp8_args& a, int num_sms, cudaStream_
     const long long tiles = (long long)a.G * ((a.M + 63) / 64) * ((a.N + 127) / 128);
     if (a.M <= 32 || tiles <= 2 * num_sms) return launch_gemm_mx_few(a, p, num_sms, s);
     switch (a.out_dtype) {
-        case RM_F32: return launch_tile<RM_F32>(a, p, num_sms, s);
-        case RM_BF16: return launch_tile<RM_BF16>(a, p, num_sms, s);
-        default: return launch_tile<RM_E4M3>(a, p, num_sms, s);
+        case RM_F32: return launch_out<RM_F32>(a, p, num_sms, s);
+        case RM_BF16: return launch_out<RM_BF16>(a, p, num_sms, s);
+        default: return launch_out<RM_E4M3>(a, p, num_sms, s);
     }
 }
 
