@@ -31,12 +31,13 @@ namespace {
 constexpr int BM = 128;            // rows of a CTA
 constexpr int TM = 2 * BM, BN = 256;   // the pair's tile
 constexpr int BK = 128;            // K elements (bytes) of a ring stage
+constexpr int kBand = 8;            // tile rows that are worked down together
 constexpr int kSlots = 4;          // chunks (512 of K) of scale atoms in shared memory ...
 constexpr int kTSlots = 2;         // ... and in tensor memory
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = (4 + kEpiWarps) * 32;
-constexpr int kOutBytes = 8192;    // staging of an epilogue warp's output
 
+template <int OUT>
 struct Cfg {
     static constexpr int B_ROWS = BN / 2;                  // W rows a CTA loads
     static constexpr int A_BYTES = BM * BK, B_BYTES = B_ROWS * BK;
@@ -44,14 +45,18 @@ struct Cfg {
     static constexpr int B_ATOMS = BN / 128;               // every CTA holds all BN columns' scales
     static constexpr int SLOT_BYTES = 512 * (1 + B_ATOMS);
     static constexpr int SLOT_COLS = 4 * (1 + B_ATOMS);
-    static constexpr int EPI_BYTES = kEpiWarps * (kOutBytes + 512);   // staging and bias of each epilogue warp
+    // Staging of an epilogue warp's output: two boxes of 32 rows x 128 bytes of
+    // fp32, which is bound by its stores; else one (two of 16 rows for e4m3), so
+    // that a fifth ring stage fits (8192 x 8192 x 8192: 2930 -> 3120 TFLOP/s).
+    static constexpr int OUT_BYTES = OUT == RM_F32 ? 8192 : 4096;
+    static constexpr int EPI_BYTES = kEpiWarps * (OUT_BYTES + 512);   // staging and bias of the epilogue warps
     static constexpr int STAGES_RAW = (227 * 1024 - 1024 - 512 - kSlots * SLOT_BYTES - EPI_BYTES) / STAGE_BYTES;
     static constexpr int STAGES = STAGES_RAW > 8 ? 8 : STAGES_RAW;
-    static constexpr int NBARS = 2 * STAGES + 2 * kSlots + 4;
+    static constexpr int NBARS = 2 * STAGES + 2 * kSlots + 6;
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_BYTES + kSlots * SLOT_BYTES + 8 * NBARS + 16;
     // Accumulators: two of BN columns.  Two of 256 do not fit beside the
-    // scales: they overlap by 24 columns, which the epilogue reads first (the
-    // next tile's MMAs wait for those alone).
+    // scales: they overlap by 24 columns, which the epilogue reads before the
+    // rest (of the present tile's, the next tile's MMAs wait for those alone).
     static constexpr int ACC1 = 232;
     static constexpr int SCALE_COL = ACC1 + BN;
     static constexpr int TMEM_COLS = SCALE_COL + kTSlots * SLOT_COLS <= 512 ? 512 : 0;
@@ -62,9 +67,13 @@ struct Tile {
     int g, m0, n0;
 };
 __device__ __forceinline__ Tile decode(uint32_t idx, uint32_t mblk, uint32_t nblk) {
-    // the M tiles of one W tile run next to each other, so that W is read from L2
-    const uint32_t col = idx / mblk, g = col / nblk;
-    return Tile{(int)g, (int)(idx - col * mblk) * TM, (int)(col - g * nblk) * BN};
+    // Bands of kBand tile rows, down each column of a band in turn: a W tile is
+    // read from L2 by the band's tiles, and the A tiles of a band stay there
+    // (8192 x 8192 x 8192: 2740 TFLOP/s down whole columns, 2920 in bands of 8).
+    const uint32_t per_g = mblk * nblk, g = idx / per_g, r = idx - g * per_g;
+    const uint32_t band = r / (kBand * nblk), m0 = band * kBand, rows = min((uint32_t)kBand, mblk - m0);
+    const uint32_t q = r - m0 * nblk, nb = q / rows;
+    return Tile{(int)g, (int)(m0 + q - nb * rows) * TM, (int)nb * BN};
 }
 
 template <int OUT, int NV>
@@ -81,15 +90,16 @@ __device__ __forceinline__ void activate_all(float (&v)[NV], int act) {
 // in chunks of 64 columns, a row a thread.
 constexpr int kChunk = 64;
 
-__device__ __forceinline__ void load_rows(uint32_t taddr, float (&v)[kChunk]) {
+// Columns C0 .. C1 - 1 of the chunk.
+template <int C0, int C1>
+__device__ __forceinline__ void load_cols(uint32_t taddr, float (&v)[kChunk]) {
 #pragma unroll
-    for (int q = 0; q < kChunk / 16; ++q) {
+    for (int q = C0 / 16; q < C1 / 16; ++q) {
         float w[16];
         tmem_ld16(taddr + 16 * q, w);
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[16 * q + e] = w[e];
     }
-    tmem_ld_wait();
 }
 
 // bias (from shared memory), activation and residual of columns n .. n + 63 of
@@ -218,7 +228,7 @@ template <int OUT, bool PLAIN>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_mx_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
                    const __grid_constant__ CUtensorMap tmO, const MxParams p) {
-    using C = Cfg;
+    using C = Cfg<OUT>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     unsigned char* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
@@ -228,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE_BYTES + C::EPI_BYTES + kSlots * C::SLOT_BYTES);
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * C::STAGES;
     const uint32_t sfull0 = empty0 + 8 * C::STAGES, sempty0 = sfull0 + 8 * kSlots;
-    const uint32_t tfull0 = sempty0 + 8 * kSlots, tempty_bar = tfull0 + 16, drain_bar = tempty_bar + 8;
+    const uint32_t tfull0 = sempty0 + 8 * kSlots, tdone0 = tfull0 + 16, tover_bar = tdone0 + 16, drain_bar = tover_bar + 8;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -246,8 +256,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(tfull0 + 8 * a, 1);
+            mbar_init(tdone0 + 8 * a, 2 * kEpiWarps);
         }
-        mbar_init(tempty_bar, 2 * 32 * kEpiWarps);
+        mbar_init(tover_bar, 2 * kEpiWarps / 2);
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -312,9 +323,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             int it = 0;
             for (uint32_t idx = unit; idx < total && ok; idx += nunits, ++it) {
                 const int acc = it & 1;
-                // the last tile's epilogue has begun on every warp (so the tile before
-                // it, which had this accumulator, is done) and read the overlap
-                if (it > 0 && !warp_wait(tempty_bar, (uint32_t)(it - 1) & 1u, wc, SITE_MX_MMA)) break;
+                // the epilogues have read the accumulator's last tile, and of the tile
+                // before this one what the accumulators share
+                if ((it > 1 && !warp_wait(tdone0 + 8 * acc, (uint32_t)((it >> 1) - 1) & 1u, wc, SITE_MX_MMA)) ||
+                    (it > 0 && !warp_wait(tover_bar, (uint32_t)(it - 1) & 1u, wc, SITE_MX_MMA)))
+                    break;
                 tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(acc * C::ACC1);
                 for (int kb = 0; kb < num_kb; ++kb) {
@@ -413,10 +426,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else {
         const int quarter = warp & 3, half = (warp - 4) >> 2;
-        const uint32_t tempty_l = mapa_shared(tempty_bar, 0);
-        const uint32_t stage = out0 + (uint32_t)(warp - 4) * kOutBytes;
-        const uint32_t bias_s = out0 + kEpiWarps * kOutBytes + (uint32_t)(warp - 4) * 512u;
-        int buf = 0;   // staging buffer of the next store
+        // one arrival a warp, on the even CTA's barrier, when its tcgen05.ld have completed
+        const auto have_read = [&](uint32_t bar) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (leader) mbar_arrive(bar);
+                else mbar_arrive_cluster_relaxed(mapa_shared(bar, 0));
+            }
+        };
+        const uint32_t stage = out0 + (uint32_t)(warp - 4) * C::OUT_BYTES;
+        const uint32_t bias_s = out0 + kEpiWarps * C::OUT_BYTES + (uint32_t)(warp - 4) * 512u;
         int it = 0;
         for (uint32_t idx = unit; idx < total; idx += nunits, ++it) {
             const int acc = it & 1;
@@ -434,70 +454,80 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!warp_wait(tfull0 + 8 * acc, (uint32_t)(it >> 1) & 1u, wc, SITE_MX_EPILOGUE)) break;
             tc_fence_after();
             const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * C::ACC1 + col0);
-            const auto release = [&] {   // the columns that the next tile's accumulator overlaps have been read
-                tc_fence_before();
-                if (leader) mbar_arrive(tempty_bar);
-                else mbar_arrive_cluster_relaxed(tempty_l);
-            };
+            // the half of the columns that holds the accumulators' overlap: the last 24
+            // of the first accumulator, the first 24 of the second
+            const bool owner = acc == 0 ? half == 1 : half == 0;
             const auto store = [&](uint32_t src, int c, int r) {
                 tma_store_3d(&tmO, src, c, p.o_g_inner ? t.g : r, p.o_g_inner ? r : t.g);
             };
             if constexpr (OUT != RM_E4M3) {
-                constexpr int ESZ = OUT == RM_F32 ? 4 : 2, BOXES = ESZ / 2, BUFS = 2 / BOXES;
-                // the overlap (the last 24 columns of the first accumulator, the first 24
-                // of the second) is in the chunk that is read first
-                const int first = acc == 0 && half == 1 ? 1 : 0;
+                constexpr int BOXES = OUT == RM_F32 ? 2 : 1;   // of a chunk
+                const int first = half;   // the overlap's chunk, if this half has it
 #pragma unroll 1
                 for (int k = 0; k < 2; ++k) {
                     const int c = kChunk * (k ^ first);
                     float v[kChunk];
-                    load_rows(ta + c, v);
-                    if (k == 0) release();
+                    if (k == 0 && owner) {   // the overlap's 32 columns, then the chunk's others
+                        if (half == 1) load_cols<32, 64>(ta + c, v);
+                        else load_cols<0, 32>(ta + c, v);
+                        tmem_ld_wait();
+                        have_read(tover_bar);
+                        if (half == 1) load_cols<0, 32>(ta + c, v);
+                        else load_cols<32, 64>(ta + c, v);
+                    } else {
+                        load_cols<0, 64>(ta + c, v);
+                    }
+                    tmem_ld_wait();
+                    if (k == 1) have_read(tdone0 + 8 * acc);
                     if (row0 >= p.M || n + c >= p.N) continue;   // (one value per warp)
                     if constexpr (!PLAIN) finish_row<OUT>(v, p, bias_s + 4 * c, t.g, row0 + lane, n + c, row0 + lane < p.M);
-                    const uint32_t sb = stage + 4096u * BOXES * (uint32_t)buf;
-                    buf = buf + 1 == BUFS ? 0 : buf + 1;
-                    if (lane == 0) bulk_wait_read<BUFS - 1>();   // the buffer's last store has read it
+                    if (lane == 0) bulk_wait_read<0>();   // the last store has read the staging
                     __syncwarp();
-                    stage_rows<OUT>(v, sb, lane);
+                    stage_rows<OUT>(v, stage, lane);
                     fence_proxy_async_shared();
                     __syncwarp();
                     if (lane == 0) {
 #pragma unroll
                         for (int b = 0; b < BOXES; ++b)
-                            if (n + c + 32 * b < p.N) store(sb + 4096u * b, n + c + 32 * b, row0);
+                            if (n + c + 32 * b < p.N) store(stage + 4096u * b, n + c + 32 * b, row0);
                         bulk_commit_group();
                     }
                 }
             } else {
-                // 32-column piece with the overlap, of both halves read before anything else
-                const int shared = acc == 0 ? (half == 1 ? 3 : -1) : (half == 0 ? 0 : -1);   // (none: -1)
-                float keep[16];
+                const bool low = owner && half == 0, high = owner && half == 1;   // where the overlap's 32 columns are
+                float keep[16];   // those of the second half
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
+                    const uint32_t th = ta + ((uint32_t)(16 * h) << 16);
                     float v[kFrag];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (h == 0 || shared != j) load_piece(ta + ((uint32_t)(16 * h) << 16) + 32 * j, v + 16 * j);
-                    if (h == 0 && shared >= 0) load_piece(ta + (16u << 16) + 32u * (uint32_t)shared, keep);
-                    tmem_ld_wait();
                     if (h == 0) {
-                        release();
+                        if (owner) {
+                            if (low) load_piece(th, v);
+                            else load_piece(th + 96, v + 48);
+                            load_piece(th + (16u << 16) + (low ? 0u : 96u), keep);
+                            tmem_ld_wait();
+                            have_read(tover_bar);
+                        }
                     } else {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
-                            if (shared == 0) v[j] = keep[j];
-                            if (shared == 3) v[48 + j] = keep[j];
+                            if (low) v[j] = keep[j];
+                            if (high) v[48 + j] = keep[j];
                         }
                     }
+                    if (!low) load_piece(th, v);
+                    load_piece(th + 32, v + 16);
+                    load_piece(th + 64, v + 32);
+                    if (!high) load_piece(th + 96, v + 48);
+                    tmem_ld_wait();
+                    if (h == 1) have_read(tdone0 + 8 * acc);
                     const int r0 = row0 + 16 * h;
                     if (r0 >= p.M || n >= p.N) continue;   // (one value per warp)
                     if constexpr (!PLAIN) finish_quads(v, p, bias_s, lane);
                     float inv[2];
                     row_scales(v, inv, p, t.g, r0, n, lane);
-                    const uint32_t sb = stage + 2048u * (uint32_t)buf;
-                    buf = buf + 1 & 3;
-                    if (lane == 0) bulk_wait_read<3>();
+                    const uint32_t sb = stage + 2048u * (uint32_t)h;
+                    if (lane == 0) bulk_wait_read<1>();   // the last store from there has read it
                     __syncwarp();
                     stage_quads(v, sb, inv, lane);
                     fence_proxy_async_shared();
@@ -524,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int OUT, bool PLAIN>
 cudaError_t launch_tile(const rm_matmul_fp8_args& a, MxParams& p, int num_sms, cudaStream_t s) {
-    using C = Cfg;
+    using C = Cfg<OUT>;
     static SmemGrant grant;
     if (cudaError_t e = grant.ask(gemm_mx_kernel<OUT, PLAIN>, C::SMEM_BYTES)) return e;
     CUtensorMap ma, mw, mo;
