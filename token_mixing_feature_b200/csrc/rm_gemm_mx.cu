@@ -395,15 +395,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int r = t.m0 + (int)rank * BM + 32 * j + lane;
-                    w[0][j] = r < p.M ? scale_word(as + r * p.as_ld, ch, num_kb, p.a_vec) : 0x7f7f7f7fu;
+                    w[0][j] = scale_word(as + min(r, p.M - 1) * p.as_ld, ch, num_kb);   // (rows behind the last: any)
                 }
 #pragma unroll
                 for (int a = 0; a < C::B_ATOMS; ++a)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int r = t.n0 + 128 * a + 32 * j + lane;
-                        w[1 + a][j] =
-                            r < p.N ? scale_word(ws + (r >> p.w_shift) * p.ws_ld, ch, num_kb, p.w_vec) : 0x7f7f7f7fu;
+                        w[1 + a][j] = scale_word(ws + (min(r, p.N - 1) >> p.w_shift) * p.ws_ld, ch, num_kb);
                     }
                 // the slot is free once the MMAs that read its last content (and
                 // the tensor memory copy of it) have completed
@@ -581,11 +580,6 @@ cudaError_t launch_gemm_mx(const rm_matmul_fp8_args& a, int num_sms, cudaStream_
     p.a_scale = a.a_scale, p.as_gs = a.as_gstride, p.as_ld = a.as_ld;
     p.w_scale = a.w_scale, p.ws_gs = a.ws_gstride, p.ws_ld = a.ws_ld;
     p.w_shift = a.w_block_rows == 128 ? 7 : 0;
-    const auto quads = [](const void* b, long long x, long long y) {
-        return (reinterpret_cast<uintptr_t>(b) & 3) == 0 && x % 4 == 0 && y % 4 == 0;
-    };
-    p.a_vec = quads(a.a_scale, a.as_gstride, a.as_ld);
-    p.w_vec = quads(a.w_scale, a.ws_gstride, a.ws_ld);
     p.bias = a.bias;
     p.resid = a.resid, p.r_gs = a.r_gstride, p.r_ld = a.r_ld;
     p.o_gs = a.o_gstride, p.o_ld = a.o_ld;
@@ -602,7 +596,7 @@ cudaError_t launch_gemm_mx(const rm_matmul_fp8_args& a, int num_sms, cudaStream_
     // with 32 rows and a weight stream of many waves the few-row kernel again
     // (32 groups, N 6144, K 1536: 68 / 61).
     const long long tiles = (long long)a.G * ((a.M + 63) / 64) * ((a.N + 127) / 128);
-    if (a.M <= 32 || tiles <= 2 * num_sms) return launch_gemm_mx_few(a, p, num_sms, s);
+    if (a.M <= 32 || 2 * tiles <= 3 * num_sms) return launch_gemm_mx_few(a, p, num_sms, s);
     switch (a.out_dtype) {
         case RM_F32: return launch_out<RM_F32>(a, p, num_sms, s);
         case RM_BF16: return launch_out<RM_BF16>(a, p, num_sms, s);

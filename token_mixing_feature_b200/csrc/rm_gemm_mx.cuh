@@ -19,7 +19,6 @@ struct MxParams {
     const uint8_t* w_scale;
     long long ws_gs, ws_ld;
     int w_shift;                // row n's scales are row n >> w_shift of w_scale
-    int a_vec, w_vec;           // the scale rows start on 4-byte boundaries
     const float* bias;
     const void* resid;
     long long r_gs, r_ld;

@@ -92,12 +92,12 @@ __device__ __forceinline__ void put_row(float4 x, const MxParams& p, void* out, 
 
 // One lane's four rows of a scale atom of `rows` rows from r0 on.
 __device__ __forceinline__ uint4 atom_words(const uint8_t* s, long long ld, int shift, int r0, int rows, int lane, int chunk,
-                                            int blocks, bool vec) {
+                                            int blocks) {
     uint32_t w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int r = r0 + 32 * j + lane;
-        w[j] = r < rows ? scale_word(s + (r >> shift) * ld, chunk, blocks, vec) : 0x7f7f7f7fu;
+        w[j] = scale_word(s + (min(r, rows - 1) >> shift) * ld, chunk, blocks);   // (rows behind the last: any)
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -221,9 +221,8 @@ __global__ void __launch_bounds__(kThreads)
         const long long ld = warp == 2 ? p.ws_ld : p.as_ld;
         const int shift = warp == 2 ? p.w_shift : 0, r0 = warp == 2 ? n0 : m0;
         const int rows = warp == 2 ? p.N : min(p.M, m0 + NB);
-        const bool vec = (warp == 2 ? p.w_vec : p.a_vec) && kb0 % 4 == 0;
         for (int c = 0; c < chunks; ++c) {
-            const uint4 w = atom_words(s + kb0, ld, shift, r0, rows, lane, c, nkb, vec);
+            const uint4 w = atom_words(s + kb0, ld, shift, r0, rows, lane, c, nkb);
             if (!warp_wait(sempty0 + 8 * (c % kSlots), ((uint32_t)(c / kSlots) & 1u) ^ 1u, wc, SITE_MX_SCALES)) break;
             sts128(slot0 + c % kSlots * C::SLOT_BYTES + (warp == 2 ? 0 : 512) + 16 * lane, w);
             fence_proxy_async_shared();

@@ -96,16 +96,18 @@ __device__ __forceinline__ void tc_mma_mx(uint32_t d_tmem, uint64_t a_desc, uint
 }
 
 // The 32-bit word of scales of K blocks [4 chunk, 4 chunk + 4) of one row
-// (scale 1 past the last block); vec: the row starts on a 4-byte boundary.
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int chunk, int blocks, bool vec) {
-    const int n = blocks - 4 * chunk;
+// (scale 1 past the last block), from the one or two aligned words that hold
+// them: no word without one of the row's bytes is read.  No branches, so that a
+// loader's words are on their way together (byte by byte under conditions, a
+// row length that is no multiple of four doubled a product's time).
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int chunk, int blocks) {
     const uint8_t* p = row + 4 * (long long)chunk;
-    if (vec && n >= 4) return __ldcg(reinterpret_cast<const uint32_t*>(p));
-    uint32_t w = 0x7f7f7f7fu;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (i < n) w = (w & ~(0xffu << (8 * i))) | ((uint32_t)__ldcg(p + i) << (8 * i));
-    return w;
+    const int n = min(4, blocks - 4 * chunk);
+    const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(p) & 3u;
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(p - off);
+    const uint32_t lo = __ldcg(q), hi = off + n > 4 ? __ldcg(q + 1) : 0u;
+    const uint32_t keep = 0xffffffffu >> (32 - 8 * n);
+    return (__funnelshift_r(lo, hi, 8 * off) & keep) | (0x7f7f7f7fu & ~keep);
 }
 
 // One lane of a converged warp, the same one every time.  Work issued by one
