@@ -277,6 +277,13 @@ def test_product_epilogue(rm, G, M, N, K, out, act):
     check_product(rm, M, G, M, N, K, 128, out, act, bias=True, resid=out is not torch.float8_e4m3fn)
 
 
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("G,M,N,K", [(3, 700, 592, 144), (9, 300, 784, 128), (2, 1000, 1040, 640), (20, 257, 336, 256)])
+def test_product_residual(rm, G, M, N, K, out):
+    """Large enough for the pair kernel, columns ending in every part of a tile."""
+    check_product(rm, N, G, M, N, K, 128, out, None, False, True)
+
+
 @pytest.mark.parametrize("M", [1, 8, 40, 130, 600])
 @pytest.mark.parametrize("br", [1, 128])
 def test_product_exact(rm, M, br):

@@ -37,7 +37,12 @@ constexpr int kTSlots = 2;         // ... and in tensor memory
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = (4 + kEpiWarps) * 32;
 
-template <int OUT>
+// What the epilogue does: nothing but store, bias and activation, these and the
+// residual.  (Each branch of them moves a thread's 64 values between registers,
+// taken or not.)
+enum : int { MX_PLAIN, MX_ACT, MX_RESID };
+
+template <int OUT, int EPI>
 struct Cfg {
     static constexpr int B_ROWS = BN / 2;                  // W rows a CTA loads
     static constexpr int A_BYTES = BM * BK, B_BYTES = B_ROWS * BK;
@@ -45,14 +50,15 @@ struct Cfg {
     static constexpr int B_ATOMS = BN / 128;               // every CTA holds all BN columns' scales
     static constexpr int SLOT_BYTES = 512 * (1 + B_ATOMS);
     static constexpr int SLOT_COLS = 4 * (1 + B_ATOMS);
-    // Staging of an epilogue warp's output: two boxes of 32 rows x 128 bytes of
-    // fp32, which is bound by its stores; else one (two of 16 rows for e4m3), so
-    // that a fifth ring stage fits (8192 x 8192 x 8192: 2930 -> 3120 TFLOP/s).
-    static constexpr int OUT_BYTES = OUT == RM_F32 ? 8192 : 4096;
+    // Staging of an epilogue warp's output: two boxes of 32 rows x 128 bytes for
+    // fp32, which is bound by its stores, and where the residual arrives there;
+    // else one (two of 16 rows for e4m3), so that a fifth ring stage fits (8192 x
+    // 8192 x 8192: 2930 -> 3120 TFLOP/s).
+    static constexpr int OUT_BYTES = OUT == RM_F32 || EPI == MX_RESID ? 8192 : 4096;
     static constexpr int EPI_BYTES = kEpiWarps * (OUT_BYTES + 512);   // staging and bias of the epilogue warps
     static constexpr int STAGES_RAW = (227 * 1024 - 1024 - 512 - kSlots * SLOT_BYTES - EPI_BYTES) / STAGE_BYTES;
     static constexpr int STAGES = STAGES_RAW > 8 ? 8 : STAGES_RAW;
-    static constexpr int NBARS = 2 * STAGES + 2 * kSlots + 6;
+    static constexpr int NBARS = 2 * STAGES + 2 * kSlots + 6 + (EPI == MX_RESID ? 2 * kEpiWarps : 0);
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_BYTES + kSlots * SLOT_BYTES + 8 * NBARS + 16;
     // Accumulators: two of BN columns.  Two of 256 do not fit beside the
     // scales: they overlap by 24 columns, which the epilogue reads before the
@@ -102,11 +108,9 @@ __device__ __forceinline__ void load_cols(uint32_t taddr, float (&v)[kChunk]) {
     }
 }
 
-// bias (from shared memory), activation and residual of columns n .. n + 63 of
-// row m (live: it exists), in place.
+// bias (from shared memory) and activation, in place.
 template <int OUT>
-__device__ __forceinline__ void finish_row(float (&v)[kChunk], const MxParams& p, uint32_t bias, int g, int m, int n,
-                                           bool live) {
+__device__ __forceinline__ void finish_row(float (&v)[kChunk], const MxParams& p, uint32_t bias) {
     if (p.bias) {
 #pragma unroll
         for (int q = 0; q < kChunk / 4; ++q) {
@@ -117,16 +121,21 @@ __device__ __forceinline__ void finish_row(float (&v)[kChunk], const MxParams& p
         }
     }
     activate_all<OUT>(v, p.act);
-    if (p.resid && live) {
-        constexpr int E = OUT == RM_F32 ? 4 : 8;   // elements of a 16-byte vector
-        const char* r = static_cast<const char*>(p.resid) + (g * p.r_gs + m * p.r_ld + n) * (16 / E);
+}
+
+// The residual's boxes in the staging buffer, added to the chunk.
+template <int OUT>
+__device__ __forceinline__ void add_rows(float (&v)[kChunk], uint32_t buf, int lane) {
+    constexpr int E = OUT == RM_F32 ? 4 : 8;   // elements of a 16-byte vector
+    const uint32_t row = buf + 128u * (uint32_t)lane, sw = (uint32_t)(lane & 7);
 #pragma unroll
-        for (int q = 0; q < kChunk / E; ++q) {
-            if (n + E * q >= p.N) break;   // (N is a multiple of 16)
-            float2 f[E / 2];
-            unpack_pairs(reinterpret_cast<const uint4*>(r)[q], f);
+    for (int j = 0; j < kChunk / E; ++j) {
+        float2 f[E / 2];
+        unpack_pairs(lds128(row + 4096u * (uint32_t)(j / 8) + (((uint32_t)(j % 8) ^ sw) << 4)), f);
 #pragma unroll
-            for (int e = 0; e < E / 2; ++e) v[E * q + 2 * e] += f[e].x, v[E * q + 2 * e + 1] += f[e].y;
+        for (int e = 0; e < E / 2; ++e) {
+            const float2 y = f2_add(make_float2(v[E * j + 2 * e], v[E * j + 2 * e + 1]), f[e]);
+            v[E * j + 2 * e] = y.x, v[E * j + 2 * e + 1] = y.y;
         }
     }
 }
@@ -222,13 +231,12 @@ __device__ __forceinline__ void stage_quads(const float (&v)[kFrag], uint32_t bu
     }
 }
 
-// PLAIN: no bias, activation or residual (each of their branches moves the 64
-// values of a thread between registers, untaken or not).
-template <int OUT, bool PLAIN>
+template <int OUT, int EPI>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_mx_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
-                   const __grid_constant__ CUtensorMap tmO, const MxParams p) {
-    using C = Cfg<OUT>;
+                   const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmR, const MxParams p) {
+    using C = Cfg<OUT, EPI>;
+    constexpr bool PLAIN = EPI == MX_PLAIN;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     unsigned char* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
@@ -238,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE_BYTES + C::EPI_BYTES + kSlots * C::SLOT_BYTES);
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * C::STAGES;
     const uint32_t sfull0 = empty0 + 8 * C::STAGES, sempty0 = sfull0 + 8 * kSlots;
-    const uint32_t tfull0 = sempty0 + 8 * kSlots, tdone0 = tfull0 + 16, tover_bar = tdone0 + 16, drain_bar = tover_bar + 8;
+    const uint32_t tfull0 = sempty0 + 8 * kSlots, tdone0 = tfull0 + 16, tover_bar = tdone0 + 16, drain_bar = tover_bar + 8, rbar0 = drain_bar + 8;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -260,11 +268,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(tover_bar, 2 * kEpiWarps / 2);
         mbar_init(drain_bar, 1);
+        if (EPI == MX_RESID)
+            for (int i = 0; i < 2 * kEpiWarps; ++i) mbar_init(rbar0 + 8 * i, 1);
         *abort_flag = 0;
         fence_mbar_init();
         prefetch_tmap(&tmA);
         prefetch_tmap(&tmW);
         prefetch_tmap(&tmO);
+        if (EPI == MX_RESID) prefetch_tmap(&tmR);
     }
     if (warp == 0) {
         tmem_alloc_pair(smem_u32(tmem_slot), C::TMEM_COLS);
@@ -436,6 +447,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         const uint32_t stage = out0 + (uint32_t)(warp - 4) * C::OUT_BYTES;
         const uint32_t bias_s = out0 + kEpiWarps * C::OUT_BYTES + (uint32_t)(warp - 4) * 512u;
+        constexpr int BOXES = OUT == RM_F32 ? 2 : 1;   // of a chunk (bf16, fp32)
+        // The residual's boxes come to the staging buffer that their results leave
+        // from: fetch(b, ..) loads the one at column c into buffer b, if there is one
+        // (all earlier stores have read theirs); `due` has a bit for each on its way.
+        const uint32_t rbar = rbar0 + 16u * (uint32_t)(warp - 4);
+        uint32_t due = 0, rphase = 0;
+        const auto fetch = [&](int b, int c, int row0, int g) {
+            if (row0 >= p.M || c >= p.N) return;
+            if (lane == 0) {
+                bulk_wait_read<0>();
+                mbar_arrive_expect_tx(rbar + 8 * b, 4096);
+                tma_load_3d(stage + 4096u * b, &tmR, rbar + 8 * b, c, p.r_g_inner ? g * p.r_gmul : row0,
+                            p.r_g_inner ? row0 : g * p.r_gmul);
+            }
+            due |= 1u << b;
+        };
+        const auto arrived = [&](int b, bool honour_abort) {
+            const bool ok = __all_sync(0xffffffffu, mbar_wait(rbar + 8 * b, rphase >> b & 1u, wc, SITE_MX_EPILOGUE, honour_abort));
+            rphase ^= 1u << b;
+            due &= ~(1u << b);
+            return ok;
+        };
         int it = 0;
         for (uint32_t idx = unit; idx < total; idx += nunits, ++it) {
             const int acc = it & 1;
@@ -450,6 +483,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                       __float_as_uint(x.w)));
                 __syncwarp();
             }
+            if constexpr (EPI == MX_RESID) {   // the tile's first two boxes of it
+                const int c = kChunk * half;
+                fetch(0, n + c, row0, t.g);
+                fetch(1, n + (BOXES == 2 ? c + 32 : c ^ kChunk), row0, t.g);
+            }
             if (!warp_wait(tfull0 + 8 * acc, (uint32_t)(it >> 1) & 1u, wc, SITE_MX_EPILOGUE)) break;
             tc_fence_after();
             const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * C::ACC1 + col0);
@@ -460,8 +498,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_store_3d(&tmO, src, c, p.o_g_inner ? t.g : r, p.o_g_inner ? r : t.g);
             };
             if constexpr (OUT != RM_E4M3) {
-                constexpr int BOXES = OUT == RM_F32 ? 2 : 1;   // of a chunk
                 const int first = half;   // the overlap's chunk, if this half has it
+                bool ok = true;
 #pragma unroll 1
                 for (int k = 0; k < 2; ++k) {
                     const int c = kChunk * (k ^ first);
@@ -478,20 +516,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tmem_ld_wait();
                     if (k == 1) have_read(tdone0 + 8 * acc);
-                    if (row0 >= p.M || n + c >= p.N) continue;   // (one value per warp)
-                    if constexpr (!PLAIN) finish_row<OUT>(v, p, bias_s + 4 * c, t.g, row0 + lane, n + c, row0 + lane < p.M);
-                    if (lane == 0) bulk_wait_read<0>();   // the last store has read the staging
-                    __syncwarp();
-                    stage_rows<OUT>(v, stage, lane);
-                    fence_proxy_async_shared();
-                    __syncwarp();
-                    if (lane == 0) {
+                    if (row0 < p.M && n + c < p.N) {   // (one value per warp)
+                        if constexpr (!PLAIN) finish_row<OUT>(v, p, bias_s + 4 * c);
+                        uint32_t to = stage;
+                        if constexpr (EPI == MX_RESID) {
+                            to += BOXES == 1 ? 4096u * (uint32_t)k : 0u;
 #pragma unroll
-                        for (int b = 0; b < BOXES; ++b)
-                            if (n + c + 32 * b < p.N) store(stage + 4096u * b, n + c + 32 * b, row0);
-                        bulk_commit_group();
+                            for (int b = 0; b < BOXES; ++b)
+                                if (n + c + 32 * b < p.N) ok = arrived(BOXES == 1 ? k : b, true) && ok;
+                            if (!ok) break;
+                            add_rows<OUT>(v, to, lane);
+                        } else {
+                            if (lane == 0) bulk_wait_read<0>();   // the last store has read the staging
+                            __syncwarp();
+                        }
+                        stage_rows<OUT>(v, to, lane);
+                        fence_proxy_async_shared();
+                        __syncwarp();
+                        if (lane == 0) {
+#pragma unroll
+                            for (int b = 0; b < BOXES; ++b)
+                                if (n + c + 32 * b < p.N) store(to + 4096u * b, n + c + 32 * b, row0);
+                            bulk_commit_group();
+                        }
+                    }
+                    if constexpr (EPI == MX_RESID && BOXES == 2) {   // the other chunk's boxes
+                        if (k == 0) {
+                            fetch(0, n + (c ^ kChunk), row0, t.g);
+                            fetch(1, n + (c ^ kChunk) + 32, row0, t.g);
+                        }
                     }
                 }
+                if (!ok) break;
             } else {
                 const bool low = owner && half == 0, high = owner && half == 1;   // where the overlap's 32 columns are
                 float keep[16];   // those of the second half
@@ -538,6 +594,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
+        for (int b = 0; b < 2; ++b)   // (a wait ran out: copies land before shared memory goes away)
+            if (due >> b & 1u) arrived(b, false);
         if (lane == 0) bulk_wait_all();
         __syncwarp();
     }
@@ -551,25 +609,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int OUT, bool PLAIN>
+template <int OUT, int EPI>
 cudaError_t launch_tile(const rm_matmul_fp8_args& a, MxParams& p, int num_sms, cudaStream_t s) {
-    using C = Cfg<OUT>;
+    using C = Cfg<OUT, EPI>;
     static SmemGrant grant;
-    if (cudaError_t e = grant.ask(gemm_mx_kernel<OUT, PLAIN>, C::SMEM_BYTES)) return e;
-    CUtensorMap ma, mw, mo;
+    if (cudaError_t e = grant.ask(gemm_mx_kernel<OUT, EPI>, C::SMEM_BYTES)) return e;
+    CUtensorMap ma, mw, mo, mr = {};
     const int osz = OUT == RM_F32 ? 4 : OUT == RM_BF16 ? 2 : 1, orows = OUT == RM_E4M3 ? 16 : 32;
     if (!matrix_map(&ma, a.A, a.K, a.M, a.G, a.a_ld, a.a_gstride, 1, BM, &p.a_g_inner, &p.a_gmul) ||
         !matrix_map(&mw, a.W, a.K, a.N, a.G, a.w_ld, a.w_gstride, 1, C::B_ROWS, &p.w_g_inner, &p.w_gmul) ||
         !matrix_map(&mo, a.out, a.N, a.M, a.G, a.o_ld, a.o_gstride, osz, orows, &p.o_g_inner, nullptr))
         return cudaErrorInvalidValue;
+    if (EPI == MX_RESID &&
+        !matrix_map(&mr, a.resid, a.N, a.M, a.G, a.r_ld, a.r_gstride, osz, orows, &p.r_g_inner, &p.r_gmul))
+        return cudaErrorInvalidValue;
     const long long tiles = (long long)a.G * ((a.M + TM - 1) / TM) * ((a.N + BN - 1) / BN);
     const int units = (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
-    return launch_cluster(gemm_mx_kernel<OUT, PLAIN>, dim3(units * 2), kThreads, C::SMEM_BYTES, 2, s, ma, mw, mo, p);
+    return launch_cluster(gemm_mx_kernel<OUT, EPI>, dim3(units * 2), kThreads, C::SMEM_BYTES, 2, s, ma, mw, mo, mr, p);
 }
 template <int OUT>
 cudaError_t launch_out(const rm_matmul_fp8_args& a, MxParams& p, int num_sms, cudaStream_t s) {
-    const bool plain = !a.bias && !a.resid && a.act == RM_ACT_NONE;
-    return plain ? launch_tile<OUT, true>(a, p, num_sms, s) : launch_tile<OUT, false>(a, p, num_sms, s);
+    if constexpr (OUT != RM_E4M3)
+        if (a.resid) return launch_tile<OUT, MX_RESID>(a, p, num_sms, s);
+    if (a.bias || a.act != RM_ACT_NONE) return launch_tile<OUT, MX_ACT>(a, p, num_sms, s);
+    return launch_tile<OUT, MX_PLAIN>(a, p, num_sms, s);
 }
 
 }  // namespace

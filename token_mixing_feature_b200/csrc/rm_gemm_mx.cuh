@@ -21,8 +21,9 @@ struct MxParams {
     int w_shift;                // row n's scales are row n >> w_shift of w_scale
     const float* bias;
     const void* resid;
-    long long r_gs, r_ld;
-    int o_g_inner;              // map coordinate order of out (pair kernel)
+    long long r_gs, r_ld;       // (few-row kernel)
+    int o_g_inner, r_g_inner;   // map coordinate orders of out and resid (pair kernel)
+    int r_gmul;
     long long o_gs, o_ld;       // (few-row kernel)
     uint8_t* out_scale;
     long long os_gs, os_ld;
