@@ -22,10 +22,10 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ uint32_t max16(uint32_t m) {   // over the 16 lanes of a row
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    return m;
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
 // 8 x 8 elements as they were loaded, and the largest magnitude bits of a row,
@@ -44,8 +44,8 @@ struct Patch<__nv_bfloat16> {
     }
     // two 16-bit magnitudes an instruction; as fp32 bits they are the high halves
     __device__ __forceinline__ uint32_t row_max(int r) const {
-        const uint32_t m = __vmaxu2(__vmaxu2(u[r].x & 0x7fff7fffu, u[r].y & 0x7fff7fffu),
-                                    __vmaxu2(u[r].z & 0x7fff7fffu, u[r].w & 0x7fff7fffu));
+        const uint32_t m = max_u16x2(max_u16x2(u[r].x & 0x7fff7fffu, u[r].y & 0x7fff7fffu),
+                                    max_u16x2(u[r].z & 0x7fff7fffu, u[r].w & 0x7fff7fffu));
         return max(m << 16, m & 0xffff0000u);
     }
     __device__ __forceinline__ void col_max(uint32_t (&m)[8]) const {
@@ -53,7 +53,7 @@ struct Patch<__nv_bfloat16> {
         for (int i = 0; i < 4; ++i) {
             uint32_t v = 0;
 #pragma unroll
-            for (int r = 0; r < 8; ++r) v = __vmaxu2(v, word(r, i) & 0x7fff7fffu);
+            for (int r = 0; r < 8; ++r) v = max_u16x2(v, word(r, i) & 0x7fff7fffu);
             m[2 * i] = v << 16, m[2 * i + 1] = v & 0xffff0000u;
         }
     }
@@ -106,12 +106,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 2 ? 4 : 2) quant_block_
     __shared__ __align__(8) uint8_t cbyte[kBlk];
     __shared__ __align__(16) unsigned char turn[kBlk * kBlk];
     pdl_enter();
-    const int tcol = (p.cols + kBlk - 1) / kBlk, trow = (p.rows + kBlk - 1) / kBlk;
-    long long tile = blockIdx.x;
-    const int cb = (int)(tile % tcol);
-    tile /= tcol;
-    const int rb = (int)(tile % trow);
-    const long long g = tile / trow;
+    const uint32_t tcol = (uint32_t)(p.cols + kBlk - 1) / kBlk, trow = (uint32_t)(p.rows + kBlk - 1) / kBlk;
+    const uint32_t tr = blockIdx.x / tcol;
+    const int cb = (int)(blockIdx.x - tr * tcol), rb = (int)(tr % trow);
+    const long long g = tr / trow;
     const int lane16 = threadIdx.x & 15, pr = threadIdx.x >> 4, warp = threadIdx.x >> 5;
     const int r0 = rb * kBlk + 8 * pr, c0 = cb * kBlk + 8 * lane16;
     const bool cin = c0 < p.cols;   // (cols is a multiple of 16: whole chunks)
@@ -119,8 +117,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 2 ? 4 : 2) quant_block_
     const E* src = static_cast<const E*>(p.src) + g * p.src_gs + (long long)r0 * p.src_ld + c0;
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
-        if (cin && r0 + r < p.rows) x.load(r, src + (long long)r * p.src_ld);
+        if (cin && r0 + r < p.rows) x.load(r, src);
         else x.zero(r);
+        src += p.src_ld;
     }
 
     uint32_t tb = 0;   // the tile's scale byte (TILE)
@@ -142,17 +141,26 @@ __global__ void __launch_bounds__(kThreads, sizeof(E) == 2 ? 4 : 2) quant_block_
 
     uint2 q[8];   // codes of the patch's rows
     if (TILE || p.dst) {
+        float inv = scale_inverse(tb);
+        using Max = BlockMax<8, 16>;
+        if constexpr (!TILE) {   // the eight rows' scales, row `held` in this lane
+            uint32_t m[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) m[r] = x.row_max(r);
+            const uint32_t b = scale_byte(Max::reduce(m, threadIdx.x & 31));
+            const int held = lane16 >> Max::SHIFT;
+            inv = scale_inverse(b);
+            if ((lane16 & ((1 << Max::SHIFT) - 1)) == 0 && r0 + held < p.rows)
+                p.scale[g * p.s_gs + (r0 + held) * p.s_ld + cb] = (uint8_t)b;
+        }
         uint8_t* dst = static_cast<uint8_t*>(p.dst) + g * p.dst_gs + (long long)r0 * p.dst_ld + c0;
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-            const uint32_t b = TILE ? tb : scale_byte(max16(x.row_max(r)));
-            const float inv = scale_inverse(b);
-            q[r] = make_uint2(codes4(x.at(r, 0), x.at(r, 1), x.at(r, 2), x.at(r, 3), inv),
-                              codes4(x.at(r, 4), x.at(r, 5), x.at(r, 6), x.at(r, 7), inv));
-            if (p.dst && r0 + r < p.rows) {
-                if (cin) *reinterpret_cast<uint2*>(dst + (long long)r * p.dst_ld) = q[r];
-                if (!TILE && lane16 == 0) p.scale[g * p.s_gs + (r0 + r) * p.s_ld + cb] = (uint8_t)b;
-            }
+            const float k = TILE ? inv : __shfl_sync(0xffffffffu, inv, (threadIdx.x & 16) | (r << Max::SHIFT));
+            q[r] = make_uint2(codes4(x.at(r, 0), x.at(r, 1), x.at(r, 2), x.at(r, 3), k),
+                              codes4(x.at(r, 4), x.at(r, 5), x.at(r, 6), x.at(r, 7), k));
+            if (p.dst && cin && r0 + r < p.rows) *reinterpret_cast<uint2*>(dst) = q[r];
+            dst += p.dst_ld;
         }
     }
 

@@ -106,39 +106,6 @@ struct Place {
     }
 };
 
-// The largest of each of NC values over LANES neighbouring lanes (16 or 32),
-// all NC at once: as long as a lane holds several values it gives half of them
-// away for the other lane's share of the rest.  Value i ends in the lanes whose
-// number among the LANES, without its low SHIFT bits, is i.
-template <int NC, int LANES>
-struct BlockMax {
-    static constexpr int LOGV = NC <= 1 ? 0 : NC <= 2 ? 1 : NC <= 4 ? 2 : 3, V = 1 << LOGV;
-    static constexpr int SHIFT = (LANES == 32 ? 5 : 4) - LOGV;
-    static __device__ __forceinline__ uint32_t reduce(const uint32_t (&in)[NC], int lane) {
-        uint32_t m[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) m[i] = i < NC ? in[i] : 0u;
-        int n = V;
-#pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1) {
-            if (n > 1) {
-                n >>= 1;
-                const bool up = lane & o;
-#pragma unroll
-                for (int j = 0; j < V / 2; ++j) {
-                    if (j < n) {
-                        const uint32_t keep = up ? m[j + n] : m[j], give = up ? m[j] : m[j + n];
-                        m[j] = max(keep, __shfl_xor_sync(0xffffffffu, give, o));
-                    }
-                }
-            } else {
-                m[0] = max(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
-            }
-        }
-        return m[0];
-    }
-};
-
 // gamma from shared memory where the launch gave it a place there (at the
 // ring's start): with the ring beside it, L1 holds no row's worth of it, and
 // reading it from L2 for every row doubled the traffic of wide rows.
