@@ -351,6 +351,45 @@ def test_product_not_finite(rm, M):
         assert torch.equal(o8.cpu() == 127, blocks.repeat_interleave(128, 1))
 
 
+def test_offsets_beyond_32_bits(rm):
+    """Groups 2^31 + 2^20 elements apart: the norm, the quantiser both ways and the product (few rows and many)."""
+    far = (1 << 31) + (1 << 20)
+    g = gen(11)
+    for B in (3, 400):
+        x = torch.randn(2, B, 256, generator=g).bfloat16()
+        buf = torch.empty(far + B * 256, dtype=torch.bfloat16, device="cuda")
+        v = buf.as_strided((2, B, 256), (far, 256, 1))
+        v.copy_(x)
+        n = buf.as_strided((2, 256), (far, 1))                 # two rows far apart
+        y = torch.empty(2, 256, dtype=torch.bfloat16, device="cuda")
+        rm.rm_rmsnorm_forward(n, Y=y, eps=1e-6)
+        ref, _ = R.rmsnorm(h64(x[:, 0]), np.ones(256), 1e-6)
+        assert np.all(np.abs(h64(y) - ref) <= (32 * U + R.BF16_HALF) * np.abs(ref))
+        b8 = torch.empty(far + B * 256, dtype=torch.uint8, device="cuda")
+        q, s = b8.as_strided((2, B, 256), (far, 256, 1)), torch.empty(2, B, 2, dtype=torch.uint8, device="cuda")
+        bt = torch.empty(far + 256 * up16(B), dtype=torch.uint8, device="cuda")
+        qt = bt.as_strided((2, 256, B), (far, up16(B), 1))
+        st = torch.empty(2, 256, (B + 127) // 128, dtype=torch.uint8, device="cuda")
+        rm.rm_quantize_fp8_block(v, q, s, qt, st)
+        torch.cuda.synchronize()
+        for got, gots, want in ((q, s, h64(x)), (qt, st, h64(x).swapaxes(1, 2))):
+            codes, sb = R.quantize(want, 1)
+            assert np.array_equal(codes_of(got), codes) and np.array_equal(bytes_of(gots), sb)
+        w, ws, wv = operand(g, 2, 128, 256, 128)
+        ob = torch.empty(far + B * 128, dtype=torch.bfloat16, device="cuda")
+        out = ob.as_strided((2, B, 128), (far, 128, 1))
+        rm.rm_matmul_fp8_block(q, s, w, ws, out)
+        near = torch.empty(2, B, 128, dtype=torch.bfloat16, device="cuda")
+        rm.rm_matmul_fp8_block(q.contiguous(), s, w, ws, near)
+        torch.cuda.synchronize()
+        a = R.values(codes_of(q), bytes_of(s), 1)
+        assert torch.equal(out, near)
+        tol = (2 * 256 / 32 + 64) * U * np.einsum("gmk,gnk->gmn", np.abs(a), np.abs(wv))
+        ref = np.einsum("gmk,gnk->gmn", a, wv)
+        assert np.all(np.abs(h64(out) - ref) <= tol * 1.01 + R.BF16_HALF * np.abs(ref) * 1.001)
+        del buf, b8, bt, ob
+
+
 def test_empty(rm):
     z = dict(dtype=torch.uint8, device="cuda")
     rm.rm_matmul_fp8_block(torch.empty(0, 64, **z), torch.empty(0, 1, **z), torch.empty(32, 64, **z),

@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     pdl_enter();   // operands, scales and bias may all come from the previous kernel
 
-    const WaitCtx wc{abort_flag, p.budget_ns, p.err};
+    const WaitCtx wc{abort_flag, p.budget_ns, p.err}, drain = drain_ctx(wc);
     const uint32_t mblk = (p.M + TM - 1) / TM, nblk = (p.N + BN - 1) / BN;
     const int num_kb = (p.K + BK - 1) / BK;
     const uint32_t total = (uint32_t)p.G * mblk * nblk;   // below 2^31
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (leader)   // every issued copy lands before shared memory goes away
             for (int s = 0; s < C::STAGES; ++s)
-                if (issued & (1u << s)) mbar_wait(full0 + 8 * s, (issued_phase >> s) & 1u, wc, SITE_MX_DRAIN, false);
+                if (issued & (1u << s)) mbar_wait(full0 + 8 * s, (issued_phase >> s) & 1u, drain, SITE_MX_DRAIN, false);
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (any) {   // everything issued completes before tensor memory is released
                 if (elect_one()) tc_commit_pair(drain_bar);
                 __syncwarp();
-                mbar_wait(drain_bar, 0, wc, SITE_MX_DRAIN, false);
+                mbar_wait(drain_bar, 0, drain, SITE_MX_DRAIN, false);
             }
         }
         __syncwarp();
@@ -463,8 +463,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             due |= 1u << b;
         };
-        const auto arrived = [&](int b, bool honour_abort) {
-            const bool ok = __all_sync(0xffffffffu, mbar_wait(rbar + 8 * b, rphase >> b & 1u, wc, SITE_MX_EPILOGUE, honour_abort));
+        const auto arrived = [&](int b, const WaitCtx& w, bool honour_abort) {
+            const bool ok = __all_sync(0xffffffffu, mbar_wait(rbar + 8 * b, rphase >> b & 1u, w, SITE_MX_EPILOGUE, honour_abort));
             rphase ^= 1u << b;
             due &= ~(1u << b);
             return ok;
@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             to += BOXES == 1 ? 4096u * (uint32_t)k : 0u;
 #pragma unroll
                             for (int b = 0; b < BOXES; ++b)
-                                if (n + c + 32 * b < p.N) ok = arrived(BOXES == 1 ? k : b, true) && ok;
+                                if (n + c + 32 * b < p.N) ok = arrived(BOXES == 1 ? k : b, wc, true) && ok;
                             if (!ok) break;
                             add_rows<OUT>(v, to, lane);
                         } else {
@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         for (int b = 0; b < 2; ++b)   // (a wait ran out: copies land before shared memory goes away)
-            if (due >> b & 1u) arrived(b, false);
+            if (due >> b & 1u) arrived(b, drain, false);
         if (lane == 0) bulk_wait_all();
         __syncwarp();
     }

@@ -82,6 +82,12 @@ __device__ __forceinline__ void activate(float (&v)[NV]) {
     }
 }
 
+// For waits on this CTA's own copies and MMAs in flight, which no short budget
+// may cut off: a second at the least.
+__device__ __forceinline__ WaitCtx drain_ctx(const WaitCtx& w) {
+    return WaitCtx{w.abort, w.budget_ns > 1000000000ull ? w.budget_ns : 1000000000ull, w.err};
+}
+
 // A wait of a whole warp: all lanes go on, or none.  CLUSTER: for what the
 // pair's other CTA released.
 template <bool CLUSTER = false>
@@ -98,7 +104,7 @@ inline bool matrix_map(CUtensorMap* m, const void* base, int cols, int rows, int
     if (gmul) *gmul = gs == 0 ? 0 : 1;
     if (gs == 0) G = 1;
     if (rows == 1) ld = ((long long)cols + 15) / 16 * 16;
-    if (G == 1) gs = rows * ld;
+    if (G == 1) gs = ld;
     *g_inner = gs < ld ? 1 : 0;
     return *g_inner ? make_map_e(m, base, cols, G, rows, gs * esz, ld * esz, 1, box, esz)
                     : make_map_e(m, base, cols, rows, G, ld * esz, gs * esz, box, 1, esz);

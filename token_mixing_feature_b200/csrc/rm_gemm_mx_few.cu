@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kThreads)
     if (slices > 1) cluster_arrive();   // this CTA's shared memory may be written (awaited before the partial sums)
     pdl_enter();
 
-    const WaitCtx wc{abort_flag, p.budget_ns, p.err};
+    const WaitCtx wc{abort_flag, p.budget_ns, p.err}, drain = drain_ctx(wc);
     const int mblk = (p.M + NB - 1) / NB, nblk = (p.N + BM - 1) / BM;
     const uint32_t tile = blockIdx.x >> log_slices, col = tile / (uint32_t)mblk;
     const int m0 = (int)(tile - col * (uint32_t)mblk) * NB;
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kThreads)
         // every issued copy lands before its place is used again (the MMAs have
         // waited for all of them, unless a wait ran out)
         for (int i = 0; i < C::STAGES; ++i)
-            if (issued & (1u << i)) mbar_wait(full0 + 8 * i, (issued_phase >> i) & 1u, wc, SITE_MX_DRAIN, false);
+            if (issued & (1u << i)) mbar_wait(full0 + 8 * i, (issued_phase >> i) & 1u, drain, SITE_MX_DRAIN, false);
     } else if (warp == 1) {
         constexpr uint32_t idesc0 = idesc_mx_e4m3(BM, NB, 0, 0);
         int stage = 0;
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kThreads)
     // The slice's sums: TMEM lane = column n0 + 32 warp + lane, TMEM column = row
     // of A.  Row r belongs to slice r % slices, which keeps what slice s sends of
     // its i-th row as row s * own + i of its partial results.
-    const bool drained = mbar_wait(done_bar, 0, wc, SITE_MX_EPILOGUE, false);
+    const bool drained = mbar_wait(done_bar, 0, drain, SITE_MX_EPILOGUE, false);
     const bool ok = __all_sync(0xffffffffu, drained && *abort_flag == 0);
     tc_fence_after();
     const int rows = min(NB, p.M - m0);

@@ -58,13 +58,6 @@ __device__ __forceinline__ void store_codes(char* o, const float2 (&y)[4], float
 __device__ __forceinline__ void store_codes(char* o, const float2 (&y)[2], float2 k) {
     *reinterpret_cast<uint32_t*>(o) = e4m3x4(f2_mul(y[0], k), f2_mul(y[1], k));
 }
-// 1 / sqrt(x): the approximation (2^-22.9) and a Newton step.
-__device__ __forceinline__ float inv_sqrt(float x) {
-    const float r = rsqrtf(x);
-    const float c = fmaf(-0.5f * x * r, r, 0.5f);
-    return isinf(r) || r == 0.f ? r : fmaf(r, c, r);
-}
-
 // One chunk of a global row into shared memory, asynchronously.
 __device__ __forceinline__ void copy_chunk(uint32_t dst, const char* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -189,7 +182,7 @@ __global__ void __launch_bounds__(kCta, 1) rmsnorm_kernel(const RmsNorm p, int w
             for (int i = 0; i < NC; ++i)
                 if (c0 + 32 * i < nch) x[i].store(o + i * HOP);
         }
-        const float rstd = inv_sqrt(fmaf(at.sum(sq.x + sq.y, red[par]), inv_d, p.eps));
+        const float rstd = __frsqrt_rn(fmaf(at.sum(sq.x + sq.y, red[par]), inv_d, p.eps));
         if (p.rstd && at.warp == 0 && at.lane == 0) p.rstd[row] = rstd;
         if (!p.Y && !p.Yq) continue;
         float2 y[NC][C::P];

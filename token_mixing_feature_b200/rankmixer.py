@@ -491,9 +491,9 @@ def _vec(what: str, name: str, t, dtype, n: int, device: int):
     """Address of a contiguous vector [n] (None for None)."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.shape != (n,) or t.get_device() != device or (n > 1 and t.stride(0) != 1):
-        _wrong(what, name, t, (dtype,), (n,), device)
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == (n,) and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    _wrong(what, name, t, (dtype,), (n,), device)
 
 
 def _mat(what: str, name: str, t, dtypes, shape, device: int):
@@ -501,20 +501,26 @@ def _mat(what: str, name: str, t, dtypes, shape, device: int):
     to torch or to the library."""
     if t is None:
         return None, 0
-    rows, ld = t.shape, t.stride()
-    if t.dtype not in dtypes or rows != shape or t.get_device() != device or (ld[1] != 1 and rows[1] > 1):
-        _wrong(what, name, t, dtypes, shape, device)
-    return t.data_ptr(), ld[0]
+    if t.dtype in dtypes and t.shape == shape and t.get_device() == device:
+        if t.is_contiguous():
+            return t.data_ptr(), shape[1]
+        ld = t.stride()
+        if ld[1] == 1 or shape[1] == 1:
+            return t.data_ptr(), ld[0]
+    _wrong(what, name, t, dtypes, shape, device)
 
 
 def _grp(what: str, name: str, t, dtypes, shape, device: int):
     """Address, group stride and row stride of [G, rows, cols] (None and zeros for None)."""
     if t is None:
         return None, 0, 0
-    s = t.stride()
-    if t.dtype not in dtypes or t.shape != shape or t.get_device() != device or (s[2] != 1 and shape[2] > 1):
-        _wrong(what, name, t, dtypes, shape, device)
-    return t.data_ptr(), s[0], s[1]
+    if t.dtype in dtypes and t.shape == shape and t.get_device() == device:
+        if t.is_contiguous():
+            return t.data_ptr(), shape[1] * shape[2], shape[2]
+        s = t.stride()
+        if s[2] == 1 or shape[2] == 1:
+            return t.data_ptr(), s[0], s[1]
+    _wrong(what, name, t, dtypes, shape, device)
 
 
 def _row_stream(what: str, name: str, t, rt: _Torch):
