@@ -31,7 +31,6 @@ namespace {
 constexpr int BM = 128;            // rows of a CTA
 constexpr int TM = 2 * BM, BN = 256;   // the pair's tile
 constexpr int BK = 128;            // K elements (bytes) of a ring stage
-constexpr int kBand = 8;            // tile rows that are worked down together
 constexpr int kSlots = 4;          // chunks (512 of K) of scale atoms in shared memory ...
 constexpr int kTSlots = 2;         // ... and in tensor memory
 constexpr int kEpiWarps = 8;
@@ -50,10 +49,9 @@ struct Cfg {
     static constexpr int B_ATOMS = BN / 128;               // every CTA holds all BN columns' scales
     static constexpr int SLOT_BYTES = 512 * (1 + B_ATOMS);
     static constexpr int SLOT_COLS = 4 * (1 + B_ATOMS);
-    // Staging of an epilogue warp's output: two boxes of 32 rows x 128 bytes for
-    // fp32, which is bound by its stores, and where the residual arrives there;
-    // else one (two of 16 rows for e4m3), so that a fifth ring stage fits (8192 x
-    // 8192 x 8192: 2930 -> 3120 TFLOP/s).
+    // Staging of an epilogue warp's output: a half of fp32, a chunk of bf16 (both
+    // of them where the residual arrives there), both halves of e4m3.  With 4 KB a
+    // fifth ring stage fits (8192 x 8192 x 8192: 2930 -> 3120 TFLOP/s).
     static constexpr int OUT_BYTES = OUT == RM_F32 || EPI == MX_RESID ? 8192 : 4096;
     static constexpr int EPI_BYTES = kEpiWarps * (OUT_BYTES + 512);   // staging and bias of the epilogue warps
     static constexpr int STAGES_RAW = (227 * 1024 - 1024 - 512 - kSlots * SLOT_BYTES - EPI_BYTES) / STAGE_BYTES;
@@ -72,12 +70,16 @@ struct Cfg {
 struct Tile {
     int g, m0, n0;
 };
+template <int OUT>
 __device__ __forceinline__ Tile decode(uint32_t idx, uint32_t mblk, uint32_t nblk) {
     // Bands of kBand tile rows, down each column of a band in turn: a W tile is
     // read from L2 by the band's tiles, and the A tiles of a band stay there
     // (8192 x 8192 x 8192: 2740 TFLOP/s down whole columns, 2920 in bands of 8).
+    // fp32 results are bound by writing them: bands of 2 keep the tiles in flight
+    // to fewer, whole rows (32 x 6144 x 1536 x 512: 266 -> 254 us).
+    constexpr uint32_t kBand = OUT == RM_F32 ? 2 : 8;
     const uint32_t per_g = mblk * nblk, g = idx / per_g, r = idx - g * per_g;
-    const uint32_t band = r / (kBand * nblk), m0 = band * kBand, rows = min((uint32_t)kBand, mblk - m0);
+    const uint32_t band = r / (kBand * nblk), m0 = band * kBand, rows = min(kBand, mblk - m0);
     const uint32_t q = r - m0 * nblk, nb = q / rows;
     return Tile{(int)g, (int)(m0 + q - nb * rows) * TM, (int)nb * BN};
 }
@@ -92,8 +94,8 @@ __device__ __forceinline__ void activate_all(float (&v)[NV], int act) {
     }
 }
 
-// ---- bf16 and fp32 results: an epilogue warp takes its 32 rows x 128 columns
-// in chunks of 64 columns, a row a thread.
+// ---- bf16 results: an epilogue warp takes its 32 rows x 128 columns in chunks
+// of 64 columns, a row a thread.
 constexpr int kChunk = 64;
 
 // Columns C0 .. C1 - 1 of the chunk.
@@ -109,7 +111,6 @@ __device__ __forceinline__ void load_cols(uint32_t taddr, float (&v)[kChunk]) {
 }
 
 // bias (from shared memory) and activation, in place.
-template <int OUT>
 __device__ __forceinline__ void finish_row(float (&v)[kChunk], const MxParams& p, uint32_t bias) {
     if (p.bias) {
 #pragma unroll
@@ -120,47 +121,37 @@ __device__ __forceinline__ void finish_row(float (&v)[kChunk], const MxParams& p
             v[4 * q] = lo.x, v[4 * q + 1] = lo.y, v[4 * q + 2] = hi.x, v[4 * q + 3] = hi.y;
         }
     }
-    activate_all<OUT>(v, p.act);
+    activate_all<RM_BF16>(v, p.act);
 }
 
-// The residual's boxes in the staging buffer, added to the chunk.
-template <int OUT>
+// The residual's box in the staging buffer (32 rows x 128 bytes, in the
+// 128-byte swizzle of the bulk copies), added to the chunk; and the chunk there.
 __device__ __forceinline__ void add_rows(float (&v)[kChunk], uint32_t buf, int lane) {
-    constexpr int E = OUT == RM_F32 ? 4 : 8;   // elements of a 16-byte vector
     const uint32_t row = buf + 128u * (uint32_t)lane, sw = (uint32_t)(lane & 7);
 #pragma unroll
-    for (int j = 0; j < kChunk / E; ++j) {
-        float2 f[E / 2];
-        unpack_pairs(lds128(row + 4096u * (uint32_t)(j / 8) + (((uint32_t)(j % 8) ^ sw) << 4)), f);
+    for (int j = 0; j < 8; ++j) {
+        float2 f[4];
+        unpack_pairs(lds128(row + (((uint32_t)j ^ sw) << 4)), f);
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) {
-            const float2 y = f2_add(make_float2(v[E * j + 2 * e], v[E * j + 2 * e + 1]), f[e]);
-            v[E * j + 2 * e] = y.x, v[E * j + 2 * e + 1] = y.y;
+        for (int e = 0; e < 4; ++e) {
+            const float2 y = f2_add(make_float2(v[8 * j + 2 * e], v[8 * j + 2 * e + 1]), f[e]);
+            v[8 * j + 2 * e] = y.x, v[8 * j + 2 * e + 1] = y.y;
         }
     }
 }
-
-// The chunk into boxes of 32 rows x 128 bytes (two of fp32, one of bf16), in
-// the 128-byte swizzle of the bulk stores.
-template <int OUT>
 __device__ __forceinline__ void stage_rows(const float (&v)[kChunk], uint32_t buf, int lane) {
     const uint32_t row = buf + 128u * (uint32_t)lane, sw = (uint32_t)(lane & 7);
 #pragma unroll
-    for (int j = 0; j < (OUT == RM_F32 ? 16 : 8); ++j) {
-        const uint32_t at = row + 4096u * (uint32_t)(j / 8) + (((uint32_t)(j % 8) ^ sw) << 4);
-        if constexpr (OUT == RM_F32)
-            sts128(at, make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),
-                                  __float_as_uint(v[4 * j + 3])));
-        else
-            sts128(at, make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                                  pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7])));
-    }
+    for (int j = 0; j < 8; ++j)
+        sts128(row + (((uint32_t)j ^ sw) << 4),
+               make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                          pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7])));
 }
 
-// ---- e4m3 results: two halves of 16 rows x 128 columns, 64 values a thread,
-// so that a row's 128 columns (one quantisation block) lie in the four lanes of
-// a quad.  Fragment of a half: v[4 i + 2 h + j] is row lane / 4 + 8 h, column
-// 8 i + 2 (lane % 4) + j.
+// ---- e4m3 and fp32 results: two halves of 16 rows x 128 columns, 64 values a
+// thread, so that a row's 128 columns (one quantisation block; 512 bytes of
+// fp32, which leave together) lie in the four lanes of a quad.  Fragment of a
+// half: v[4 i + 2 h + j] is row lane / 4 + 8 h, column 8 i + 2 (lane % 4) + j.
 constexpr int kFrag = 64;
 
 // A 32-column piece of 16 accumulator rows.
@@ -177,6 +168,7 @@ __device__ __forceinline__ void load_piece(uint32_t taddr, float* v) {
 }
 
 // bias (128 floats in shared memory) and activation, in place.
+template <int OUT>
 __device__ __forceinline__ void finish_quads(float (&v)[kFrag], const MxParams& p, uint32_t bias, int lane) {
     if (p.bias) {
 #pragma unroll
@@ -189,7 +181,7 @@ __device__ __forceinline__ void finish_quads(float (&v)[kFrag], const MxParams& 
             }
         }
     }
-    activate_all<RM_E4M3>(v, p.act);
+    activate_all<OUT>(v, p.act);
 }
 
 // The scale of each of the thread's two rows (its quad's largest magnitude over
@@ -229,6 +221,29 @@ __device__ __forceinline__ void stage_quads(const float (&v)[kFrag], uint32_t bu
             sts16(row + (((i / 2) ^ r7) << 4) + 8 * (i & 1) + 2 * q, __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3));
         }
     }
+}
+
+// fp32: the half in four boxes of 16 rows x 128 bytes, swizzled; the residual
+// there added, and the half put there.
+__device__ __forceinline__ uint32_t quad_at(uint32_t buf, int i, int h, int lane) {
+    const int q = lane & 3, r7 = lane >> 2;
+    return buf + 2048u * (uint32_t)(i / 4) + 128u * (uint32_t)(r7 + 8 * h) + (((2 * (i % 4) + q / 2) ^ r7) << 4) + 8 * (q & 1);
+}
+__device__ __forceinline__ void add_quads(float (&v)[kFrag], uint32_t buf, int lane) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float2 y = f2_add(make_float2(v[4 * i + 2 * h], v[4 * i + 2 * h + 1]), lds_f32x2(quad_at(buf, i, h, lane)));
+            v[4 * i + 2 * h] = y.x, v[4 * i + 2 * h + 1] = y.y;
+        }
+}
+__device__ __forceinline__ void stage_quads_f32(const float (&v)[kFrag], uint32_t buf, int lane) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            sts64(quad_at(buf, i, h, lane), make_uint2(__float_as_uint(v[4 * i + 2 * h]), __float_as_uint(v[4 * i + 2 * h + 1])));
 }
 
 template <int OUT, int EPI>
@@ -300,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t phase = 0, issued = 0, issued_phase = 0;
         bool ok = true;
         for (uint32_t idx = unit; idx < total && ok; idx += nunits) {
-            const Tile t = decode(idx, mblk, nblk);
+            const Tile t = decode<OUT>(idx, mblk, nblk);
             const int ar = t.m0 + (int)rank * BM, wr = t.n0 + (int)rank * C::B_ROWS;
             const int ag = t.g * p.a_gmul, wg = t.g * p.w_gmul;
             for (int kb = 0; kb < num_kb; ++kb) {
@@ -396,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         long long c = 0;
         bool ok = true;
         for (uint32_t idx = unit; idx < total && ok; idx += nunits) {
-            const Tile t = decode(idx, mblk, nblk);
+            const Tile t = decode<OUT>(idx, mblk, nblk);
             const uint8_t* as = p.a_scale + t.g * p.as_gs;
             const uint8_t* ws = p.w_scale + t.g * p.ws_gs;
             for (int ch = 0; ch < chunks; ++ch, ++c) {
@@ -447,19 +462,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         const uint32_t stage = out0 + (uint32_t)(warp - 4) * C::OUT_BYTES;
         const uint32_t bias_s = out0 + kEpiWarps * C::OUT_BYTES + (uint32_t)(warp - 4) * 512u;
-        constexpr int BOXES = OUT == RM_F32 ? 2 : 1;   // of a chunk (bf16, fp32)
-        // The residual's boxes come to the staging buffer that their results leave
-        // from: fetch(b, ..) loads the one at column c into buffer b, if there is one
-        // (all earlier stores have read theirs); `due` has a bit for each on its way.
+        // The residual comes to the staging buffer that its results leave from:
+        // fetch(b, ..) loads bf16's box at column c into buffer b, or fp32's four boxes
+        // from there on into the one buffer, as far as they exist (all earlier stores
+        // have read theirs); `due` has a bit for each buffer's copy on its way.
         const uint32_t rbar = rbar0 + 16u * (uint32_t)(warp - 4);
         uint32_t due = 0, rphase = 0;
         const auto fetch = [&](int b, int c, int row0, int g) {
             if (row0 >= p.M || c >= p.N) return;
             if (lane == 0) {
+                const int boxes = OUT == RM_F32 ? min(4, (p.N - c + 31) / 32) : 1;
                 bulk_wait_read<0>();
-                mbar_arrive_expect_tx(rbar + 8 * b, 4096);
-                tma_load_3d(stage + 4096u * b, &tmR, rbar + 8 * b, c, p.r_g_inner ? g * p.r_gmul : row0,
-                            p.r_g_inner ? row0 : g * p.r_gmul);
+                mbar_arrive_expect_tx(rbar + 8 * b, OUT == RM_F32 ? 2048u * (uint32_t)boxes : 4096u);
+                for (int i = 0; i < boxes; ++i)
+                    tma_load_3d(stage + (OUT == RM_F32 ? 2048u * (uint32_t)i : 4096u * (uint32_t)b), &tmR, rbar + 8 * b, c + 32 * i,
+                                p.r_g_inner ? g * p.r_gmul : row0, p.r_g_inner ? row0 : g * p.r_gmul);
             }
             due |= 1u << b;
         };
@@ -472,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int it = 0;
         for (uint32_t idx = unit; idx < total; idx += nunits, ++it) {
             const int acc = it & 1;
-            const Tile t = decode(idx, mblk, nblk);
+            const Tile t = decode<OUT>(idx, mblk, nblk);
             const int col0 = 128 * half;   // this group's 128 columns
             const int row0 = t.m0 + (int)rank * BM + quarter * 32, n = t.n0 + col0;
             if (!PLAIN && p.bias) {   // fetched while the tile's products run
@@ -483,10 +500,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                       __float_as_uint(x.w)));
                 __syncwarp();
             }
-            if constexpr (EPI == MX_RESID) {   // the tile's first two boxes of it
-                const int c = kChunk * half;
-                fetch(0, n + c, row0, t.g);
-                fetch(1, n + (BOXES == 2 ? c + 32 : c ^ kChunk), row0, t.g);
+            if constexpr (EPI == MX_RESID) {   // the tile's two chunks of it, or its first half
+                fetch(0, OUT == RM_F32 ? n : n + kChunk * half, row0, t.g);
+                if (OUT != RM_F32) fetch(1, n + (kChunk ^ kChunk * half), row0, t.g);
             }
             if (!warp_wait(tfull0 + 8 * acc, (uint32_t)(it >> 1) & 1u, wc, SITE_MX_EPILOGUE)) break;
             tc_fence_after();
@@ -497,9 +513,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const auto store = [&](uint32_t src, int c, int r) {
                 tma_store_3d(&tmO, src, c, p.o_g_inner ? t.g : r, p.o_g_inner ? r : t.g);
             };
-            if constexpr (OUT != RM_E4M3) {
+            bool ok = true;
+            if constexpr (OUT == RM_BF16) {
                 const int first = half;   // the overlap's chunk, if this half has it
-                bool ok = true;
 #pragma unroll 1
                 for (int k = 0; k < 2; ++k) {
                     const int c = kChunk * (k ^ first);
@@ -516,38 +532,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tmem_ld_wait();
                     if (k == 1) have_read(tdone0 + 8 * acc);
-                    if (row0 < p.M && n + c < p.N) {   // (one value per warp)
-                        if constexpr (!PLAIN) finish_row<OUT>(v, p, bias_s + 4 * c);
-                        uint32_t to = stage;
-                        if constexpr (EPI == MX_RESID) {
-                            to += BOXES == 1 ? 4096u * (uint32_t)k : 0u;
-#pragma unroll
-                            for (int b = 0; b < BOXES; ++b)
-                                if (n + c + 32 * b < p.N) ok = arrived(BOXES == 1 ? k : b, wc, true) && ok;
-                            if (!ok) break;
-                            add_rows<OUT>(v, to, lane);
-                        } else {
-                            if (lane == 0) bulk_wait_read<0>();   // the last store has read the staging
-                            __syncwarp();
-                        }
-                        stage_rows<OUT>(v, to, lane);
-                        fence_proxy_async_shared();
+                    if (row0 >= p.M || n + c >= p.N) continue;   // (one value per warp)
+                    if constexpr (!PLAIN) finish_row(v, p, bias_s + 4 * c);
+                    const uint32_t to = stage + (EPI == MX_RESID ? 4096u * (uint32_t)k : 0u);
+                    if constexpr (EPI == MX_RESID) {
+                        ok = arrived(k, wc, true);
+                        if (!ok) break;
+                        add_rows(v, to, lane);
+                    } else {
+                        if (lane == 0) bulk_wait_read<0>();   // the last store has read the staging
                         __syncwarp();
-                        if (lane == 0) {
-#pragma unroll
-                            for (int b = 0; b < BOXES; ++b)
-                                if (n + c + 32 * b < p.N) store(to + 4096u * b, n + c + 32 * b, row0);
-                            bulk_commit_group();
-                        }
                     }
-                    if constexpr (EPI == MX_RESID && BOXES == 2) {   // the other chunk's boxes
-                        if (k == 0) {
-                            fetch(0, n + (c ^ kChunk), row0, t.g);
-                            fetch(1, n + (c ^ kChunk) + 32, row0, t.g);
-                        }
+                    stage_rows(v, to, lane);
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        store(to, n + c, row0);
+                        bulk_commit_group();
                     }
                 }
-                if (!ok) break;
             } else {
                 const bool low = owner && half == 0, high = owner && half == 1;   // where the overlap's 32 columns are
                 float keep[16];   // those of the second half
@@ -578,21 +581,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (h == 1) have_read(tdone0 + 8 * acc);
                     const int r0 = row0 + 16 * h;
                     if (r0 >= p.M || n >= p.N) continue;   // (one value per warp)
-                    if constexpr (!PLAIN) finish_quads(v, p, bias_s, lane);
-                    float inv[2];
-                    row_scales(v, inv, p, t.g, r0, n, lane);
-                    const uint32_t sb = stage + 2048u * (uint32_t)h;
-                    if (lane == 0) bulk_wait_read<1>();   // the last store from there has read it
-                    __syncwarp();
-                    stage_quads(v, sb, inv, lane);
+                    if constexpr (!PLAIN) finish_quads<OUT>(v, p, bias_s, lane);
+                    if constexpr (OUT == RM_F32) {
+                        if constexpr (EPI == MX_RESID) {
+                            ok = arrived(0, wc, true);
+                            if (!ok) break;
+                            add_quads(v, stage, lane);
+                        } else {
+                            if (lane == 0) bulk_wait_read<0>();   // the last stores have read the staging
+                            __syncwarp();
+                        }
+                        stage_quads_f32(v, stage, lane);
+                    } else {
+                        float inv[2];
+                        row_scales(v, inv, p, t.g, r0, n, lane);
+                        if (lane == 0) bulk_wait_read<1>();
+                        __syncwarp();
+                        stage_quads(v, stage + 2048u * (uint32_t)h, inv, lane);
+                    }
                     fence_proxy_async_shared();
                     __syncwarp();
                     if (lane == 0) {
-                        store(sb, n, r0);
+                        if constexpr (OUT == RM_F32) {
+#pragma unroll
+                            for (int b = 0; b < 4; ++b)
+                                if (n + 32 * b < p.N) store(stage + 2048u * b, n + 32 * b, r0);
+                        } else {
+                            store(stage + 2048u * (uint32_t)h, n, r0);
+                        }
                         bulk_commit_group();
                     }
+                    if (EPI == MX_RESID && h == 0) fetch(0, n, row0 + 16, t.g);   // the second half's
                 }
             }
+            if (!ok) break;
         }
         for (int b = 0; b < 2; ++b)   // (a wait ran out: copies land before shared memory goes away)
             if (due >> b & 1u) arrived(b, drain, false);
@@ -615,7 +637,7 @@ cudaError_t launch_tile(const rm_matmul_fp8_args& a, MxParams& p, int num_sms, c
     static SmemGrant grant;
     if (cudaError_t e = grant.ask(gemm_mx_kernel<OUT, EPI>, C::SMEM_BYTES)) return e;
     CUtensorMap ma, mw, mo, mr = {};
-    const int osz = OUT == RM_F32 ? 4 : OUT == RM_BF16 ? 2 : 1, orows = OUT == RM_E4M3 ? 16 : 32;
+    const int osz = OUT == RM_F32 ? 4 : OUT == RM_BF16 ? 2 : 1, orows = OUT == RM_BF16 ? 32 : 16;
     if (!matrix_map(&ma, a.A, a.K, a.M, a.G, a.a_ld, a.a_gstride, 1, BM, &p.a_g_inner, &p.a_gmul) ||
         !matrix_map(&mw, a.W, a.K, a.N, a.G, a.w_ld, a.w_gstride, 1, C::B_ROWS, &p.w_g_inner, &p.w_gmul) ||
         !matrix_map(&mo, a.out, a.N, a.M, a.G, a.o_ld, a.o_gstride, osz, orows, &p.o_g_inner, nullptr))
