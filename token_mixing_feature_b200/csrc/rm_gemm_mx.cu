@@ -23,6 +23,10 @@
 //   warps 4-11  epilogue, two groups of four warps (32 accumulator rows a
 //               warp, 128 columns a group), while the next tile's MMAs run
 // All waits are bounded (rm_device.cuh).
+//
+// What bounds it: long K, the operands' way from L2 (8192 x 8192 x 8192: 3040-3120
+// TFLOP/s in a burst, 11.5 TB/s into the SMs); short K with fp32 results, writing
+// them (32 x 6144 x 1536 x 512: 236 us for 1.33 GB); in a long run, the power cap.
 #include "rm_gemm_mx.cuh"
 
 namespace rm {
@@ -54,8 +58,7 @@ struct Cfg {
     // fifth ring stage fits (8192 x 8192 x 8192: 2930 -> 3120 TFLOP/s).
     static constexpr int OUT_BYTES = OUT == RM_F32 || EPI == MX_RESID ? 8192 : 4096;
     static constexpr int EPI_BYTES = kEpiWarps * (OUT_BYTES + 512);   // staging and bias of the epilogue warps
-    static constexpr int STAGES_RAW = (227 * 1024 - 1024 - 512 - kSlots * SLOT_BYTES - EPI_BYTES) / STAGE_BYTES;
-    static constexpr int STAGES = STAGES_RAW > 8 ? 8 : STAGES_RAW;
+    static constexpr int STAGES = (227 * 1024 - 1024 - 512 - kSlots * SLOT_BYTES - EPI_BYTES) / STAGE_BYTES;
     static constexpr int NBARS = 2 * STAGES + 2 * kSlots + 6 + (EPI == MX_RESID ? 2 * kEpiWarps : 0);
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_BYTES + kSlots * SLOT_BYTES + 8 * NBARS + 16;
     // Accumulators: two of BN columns.  Two of 256 do not fit beside the
@@ -672,16 +675,16 @@ cudaError_t launch_gemm_mx(const rm_matmul_fp8_args& a, int num_sms, cudaStream_
     p.act = a.act;
     p.err = DeviceErr{a.device_status, nullptr};
     p.budget_ns = a.wait_budget_ns ? a.wait_budget_ns : 1000000000ull;
-    // Few rows, or a product whose 64 x 128 tiles are all resident at once (two
-    // CTAs an SM): the few-row kernel, which starts more CTAs and splits K.
-    // Measured, pair / few in us: G 1, M 64, N = K = 4096 15.3 / 8.5; G 1, M 256,
-    // N = K = 1536 9.6 / 8.0; 16 groups, M 128, N = K = 768 13.0 / 9.1; G 1, M 64,
-    // N 1024, K 16384 41.8 / 10.5.  Past that the pair's 256 x 256 tiles win: G 1,
-    // M 1024, N = K = 4096 17.4 / 33.8; 16 groups, M 256, N = K = 768 13.6 / 16.9;
-    // with 32 rows and a weight stream of many waves the few-row kernel again
-    // (32 groups, N 6144, K 1536: 68 / 61).
+    // Few rows, or a product of about as many 64 x 128 tiles as SMs: the few-row
+    // kernel, which starts more CTAs and splits K.  Measured, pair / few in us:
+    // one group, M 64, N = K = 4096 13.8 / 8.4; M 256, N = K = 1536 8.8 / 6.9; M 64,
+    // N 1024, K 16384 40.2 / 10.1; 8 groups, M 128, N = K = 1024 (128 tiles) 7.9 /
+    // 7.6.  Past that the pair's 256 x 256 tiles win: M 256, N 6144, K 1536 (192
+    // tiles) 9.2 / 10.0; 8 groups, M 256, N = K = 1024 (256) 8.0 / 9.0; one group, M
+    // 1024, N = K = 4096 16.3 / 33.3.  With 32 rows at the most the few-row kernel
+    // wins at any size (32 groups, N 6144, K 1536: 63.2 / 59.2; at 64 rows 65.6 / 74.3).
     const long long tiles = (long long)a.G * ((a.M + 63) / 64) * ((a.N + 127) / 128);
-    if (a.M <= 32 || 2 * tiles <= 3 * num_sms) return launch_gemm_mx_few(a, p, num_sms, s);
+    if (a.M <= 32 || 4 * tiles <= 5 * num_sms) return launch_gemm_mx_few(a, p, num_sms, s);
     switch (a.out_dtype) {
         case RM_F32: return launch_out<RM_F32>(a, p, num_sms, s);
         case RM_BF16: return launch_out<RM_BF16>(a, p, num_sms, s);

@@ -48,9 +48,10 @@ __device__ __forceinline__ float2 rcp_pair(float2 x) {
 // act(v) of a pair, without branches.  GELU's tanh form goes through
 // tanh.approx (absolute error 2^-10.9 of tanh) where the result is rounded to
 // bf16; else it is v * sigmoid(2u), u = sqrt(2/pi) (v + 0.044715 v^3) (8-bit
-// results too: the error would move codes across their borders).  The erf form takes Abramowitz and Stegun's 7.1.26,
-// erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2), t = 1 / (1 + 0.3275911 x), x >= 0,
-// whose error is at most 1.5e-7, on the side where nothing cancels.
+// results too: the error would move codes across their borders).  The erf form
+// takes Abramowitz and Stegun's 7.1.26, erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2),
+// t = 1 / (1 + 0.3275911 x), x >= 0, whose error is at most 1.5e-7, on the side
+// where nothing cancels.
 template <int ACT, bool PRECISE>
 __device__ __forceinline__ float2 activation(float2 v) {
     if constexpr (ACT == RM_ACT_GELU_TANH && !PRECISE) {

@@ -6,7 +6,8 @@
 // X by rows (forward) and by columns (weight gradient), W in 128 x 128 blocks
 // both ways (a square block is its own transpose's block, so W^T has the codes
 // and scales of W moved, and the input gradient multiplies exactly the weights
-// that the forward pass did).  HBM-bound: 2 (or 4) bytes in, 1 or 2 out.
+// that the forward pass did).  HBM-bound: 2 (or 4) bytes in, 1 or 2 out (squares
+// of 32 x 6144 x 1536 bf16 both ways: 182 us, 6.6 TB/s, the copy's rate).
 //
 // One CTA per 128 x 128 tile, 256 threads, each holding an 8 x 8 patch in
 // registers: rows 8 (t / 16) .. + 8, columns 8 (t % 16) .. + 8.  A row's 128
