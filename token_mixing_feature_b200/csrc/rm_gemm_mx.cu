@@ -485,8 +485,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         const auto arrived = [&](int b, const WaitCtx& w, bool honour_abort) {
             const bool ok = __all_sync(0xffffffffu, mbar_wait(rbar + 8 * b, rphase >> b & 1u, w, SITE_MX_EPILOGUE, honour_abort));
-            rphase ^= 1u << b;
-            due &= ~(1u << b);
+            if (ok) {
+                rphase ^= 1u << b;
+                due &= ~(1u << b);
+            }
             return ok;
         };
         int it = 0;
