@@ -284,6 +284,12 @@ def test_product_residual(rm, G, M, N, K, out):
     check_product(rm, N, G, M, N, K, 128, out, None, False, True)
 
 
+@pytest.mark.parametrize("G,M,N,K", [(300, 40, 256, 144), (150, 300, 272, 128), (90, 260, 528, 16)])
+def test_product_short_last_rows(rm, G, M, N, K):
+    """8-bit results, several tiles a CTA pair, the last 32-row part of a group with at most 16 rows: one store a tile."""
+    check_product(rm, M, G, M, N, K, 128, torch.float8_e4m3fn)
+
+
 @pytest.mark.parametrize("M", [1, 8, 40, 130, 600])
 @pytest.mark.parametrize("br", [1, 128])
 def test_product_exact(rm, M, br):

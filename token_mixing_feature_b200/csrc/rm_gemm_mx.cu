@@ -491,6 +491,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             return ok;
         };
+        // e4m3: the two staging buffers by turns, one a store that is made (a half
+        // behind the last row makes none, so its number does not tell the buffer)
+        uint32_t codes = 0;
         int it = 0;
         for (uint32_t idx = unit; idx < total; idx += nunits, ++it) {
             const int acc = it & 1;
@@ -600,9 +603,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else {
                         float inv[2];
                         row_scales(v, inv, p, t.g, r0, n, lane);
-                        if (lane == 0) bulk_wait_read<1>();
+                        if (lane == 0) bulk_wait_read<1>();   // the store before the last has read its buffer
                         __syncwarp();
-                        stage_quads(v, stage + 2048u * (uint32_t)h, inv, lane);
+                        stage_quads(v, stage + codes, inv, lane);
                     }
                     fence_proxy_async_shared();
                     __syncwarp();
@@ -612,10 +615,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int b = 0; b < 4; ++b)
                                 if (n + 32 * b < p.N) store(stage + 2048u * b, n + 32 * b, r0);
                         } else {
-                            store(stage + 2048u * (uint32_t)h, n, r0);
+                            store(stage + codes, n, r0);
                         }
                         bulk_commit_group();
                     }
+                    codes ^= 2048u;
                     if (EPI == MX_RESID && h == 0) fetch(0, n, row0 + 16, t.g);   // the second half's
                 }
             }
