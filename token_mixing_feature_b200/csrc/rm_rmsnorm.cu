@@ -390,14 +390,13 @@ __global__ void __launch_bounds__(1024) colsum_parts_kernel(const float* part, f
 struct Shape {
     int nc, warps, groups, threads, stages, grid, gamma_bytes;
     size_t smem;
-    Shape(long long rows, int D, int esz, int inputs, bool gamma, int max_nc) {
+    Shape(long long rows, int D, int esz, int inputs, bool gamma, int aim) {
         const int most = (D * esz / 16 + 31) / 32;
         const size_t row_bytes = (size_t)D * esz * inputs;
-        // Warps a row: as few as hold it in max_nc chunks a thread (what a row
-        // costs besides, its sum and its waits, is shared by those), but as many as
-        // there are chunks for where the SMs have a row each.
-        warps = std::min(rows <= kSms ? most : (most + max_nc - 1) / max_nc, kCta / 32);
-        nc = (most + warps - 1) / warps;
+        // Groups: as many as there are warps for with `aim` chunks a thread (what
+        // a row costs besides, its sum and its waits, is shared by those), as rows an
+        // SM, and as the ring has room for.
+        warps = std::min((most + aim - 1) / aim, kCta / 32);
         groups = kCta / 32 / warps;
         if (warps > 1) groups = std::min(groups, 15);   // (named barriers)
         groups = (int)std::min<long long>(groups, (rows + kSms - 1) / kSms);
@@ -407,6 +406,11 @@ struct Shape {
         // gamma in shared memory where several rows use it and no group gives way
         gamma_bytes = gamma && rows > 2 * kSms && with == without ? 4 * D : 0;
         groups = without;
+        // the warps that this leaves go to the rows (gradient of 4099 x 7184 fp32, one
+        // group: 8 warps 132 us, 15 85 us; of 160 x 1536 bf16 6.1 / 5.1)
+        warps = std::min(most, kCta / 32 / groups);
+        nc = (most + warps - 1) / warps;
+        warps = (most + nc - 1) / nc;
         stages = (int)std::min<size_t>(4, (kRing - gamma_bytes) / (row_bytes * groups));
         threads = groups * warps * 32;
         smem = gamma_bytes + row_bytes * groups * stages;
@@ -414,11 +418,15 @@ struct Shape {
     }
 };
 
-// Chunks a thread at most (what the registers hold without spilling).
+// Chunks a thread at most (what the registers hold without spilling).  fp32
+// gradients want half of that where a row has warps for it (8192 x 4096: 8 chunks
+// 114 us, 4 75 us); the other way round, forward fp32 rows 33 with 8, 42 with 4
+// (4099 x 7184).
 template <typename E>
 constexpr int kFwdChunks = sizeof(E) == 2 ? 6 : 8;
 template <typename E>
 constexpr int kBwdChunks = sizeof(E) == 2 ? 4 : 8;
+constexpr int kBwdAim = 4;
 
 template <typename E, int NC, bool RESID>
 cudaError_t fwd(const RmsNorm& p, const Shape& sh, cudaStream_t s) {
@@ -451,7 +459,7 @@ cudaError_t bwd(const RmsNormGrad& p, const Shape& sh, cudaStream_t s) {
 
 template <typename E>
 cudaError_t bwd_e(const RmsNormGrad& p, int* parts, cudaStream_t s) {
-    const Shape sh(p.rows, p.D, sizeof(E), p.dSum ? 3 : 2, p.gamma != nullptr, kBwdChunks<E>);
+    const Shape sh(p.rows, p.D, sizeof(E), p.dSum ? 3 : 2, p.gamma != nullptr, kBwdAim);
     *parts = sh.grid;
     switch (sh.nc) {
         case 1: return bwd<E, 1>(p, sh, s);
