@@ -284,6 +284,14 @@ def test_product_residual(rm, G, M, N, K, out):
     check_product(rm, N, G, M, N, K, 128, out, None, False, True)
 
 
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32, torch.float8_e4m3fn])
+@pytest.mark.parametrize("G,M,N,K,br,act", [(9, 300, 784, 700, 128, None), (9, 300, 784, 400, 128, "tanh"),
+                                            (3, 1000, 784, 640, 1, "erf"), (3, 1000, 784, 16, 1, "relu")])
+def test_product_many_tiles(rm, G, M, N, K, br, out, act):
+    """More 64 x 128 tiles than fit on the GPU at once: the pair kernel for every type and activation."""
+    check_product(rm, K, G, M, N, K, br, out, act, bias=act is not None, resid=act == "erf" and out is not torch.float8_e4m3fn)
+
+
 @pytest.mark.parametrize("G,M,N,K", [(300, 40, 256, 144), (150, 300, 272, 128), (90, 260, 528, 16)])
 def test_product_short_last_rows(rm, G, M, N, K):
     """8-bit results, several tiles a CTA pair, the last 32-row part of a group with at most 16 rows: one store a tile."""

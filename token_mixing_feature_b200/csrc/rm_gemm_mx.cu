@@ -681,16 +681,25 @@ cudaError_t launch_gemm_mx(const rm_matmul_fp8_args& a, int num_sms, cudaStream_
     p.act = a.act;
     p.err = DeviceErr{a.device_status, nullptr};
     p.budget_ns = a.wait_budget_ns ? a.wait_budget_ns : 1000000000ull;
-    // Few rows, or a product of about as many 64 x 128 tiles as SMs: the few-row
-    // kernel, which starts more CTAs and splits K.  Measured, pair / few in us:
-    // one group, M 64, N = K = 4096 13.8 / 8.4; M 256, N = K = 1536 8.8 / 6.9; M 64,
-    // N 1024, K 16384 40.2 / 10.1; 8 groups, M 128, N = K = 1024 (128 tiles) 7.9 /
-    // 7.6.  Past that the pair's 256 x 256 tiles win: M 256, N 6144, K 1536 (192
-    // tiles) 9.2 / 10.0; 8 groups, M 256, N = K = 1024 (256) 8.0 / 9.0; one group, M
-    // 1024, N = K = 4096 16.3 / 33.3.  With 32 rows at the most the few-row kernel
-    // wins at any size (32 groups, N 6144, K 1536: 63.2 / 59.2; at 64 rows 65.6 / 74.3).
+    // Few rows, or at most one 64 x 128 tile an SM: the few-row kernel, which
+    // starts more CTAs and splits K.  Measured, pair / few in us: M 64, N = K = 4096
+    // 13.8 / 8.4; M 64, N 1024, K 16384 40.2 / 10.1; 8 groups, M 128, N 1024 (128
+    // tiles), K 1024 8.1 / 7.5, K 4096 15.0 / 12.4.  Past that K is not split and the
+    // pair's 256 x 256 tiles win: 5 groups, M 256, N 1104 (180 tiles), K 1024 8.1 /
+    // 8.3, K 4096 15.0 / 16.8; M 1024, N = K = 4096 16.3 / 33.3.  With 32 rows at the
+    // most the few-row kernel wins at any size (32 groups, N 6144, K 1536: 63.2 /
+    // 59.2; at 64 rows 65.6 / 74.3).
+    //
+    // Where the epilogue is long (other results than bf16, GELU) and K is not, it
+    // wins as long as its tiles are one wave, two on an SM: 8 groups, M 256, N 1024
+    // (256 tiles), K 1024: fp32 9.9 / 8.4, bf16 with GELU 10.8 / 9.6, e4m3 9.2 / 9.2,
+    // with GELU 11.4 / 9.9; K 256: 8.1 / 6.1, 8.9 / 7.4, 7.3 / 6.8, 9.4 / 7.5; K 2048:
+    // 12.6 / 11.4, 13.4 / 12.7, 11.8 / 12.2, 13.8 / 12.8.  A second wave loses (320
+    // tiles, K 256, bf16: 6.7 / 10.2).
     const long long tiles = (long long)a.G * ((a.M + 63) / 64) * ((a.N + 127) / 128);
-    if (a.M <= 32 || 4 * tiles <= 5 * num_sms) return launch_gemm_mx_few(a, p, num_sms, s);
+    const bool finish = a.out_dtype != RM_BF16 || a.act == RM_ACT_GELU_TANH || a.act == RM_ACT_GELU_ERF;
+    const bool one_wave = tiles <= (finish && a.K <= 2048 ? 2 : 1) * num_sms;
+    if (a.M <= 32 || one_wave) return launch_gemm_mx_few(a, p, num_sms, s);
     switch (a.out_dtype) {
         case RM_F32: return launch_out<RM_F32>(a, p, num_sms, s);
         case RM_BF16: return launch_out<RM_BF16>(a, p, num_sms, s);
