@@ -96,6 +96,13 @@ def test_norm(rm, rows, D, dtype):
     R.assert_quantized(codes_of(q2), bytes_of(s2), ref1, 32 * U * np.abs(ref1), "norm without gamma")
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,D", [(9001, 80), (5001, 256), (3001, 1536), (1201, 3600), (700, 7184), (310, 16384)])
+def test_norm_many_rows(rm, rows, D, dtype):
+    """Every group walks over several rows (the ring's places are used again), gamma kept in shared memory."""
+    test_norm(rm, rows, D, dtype)
+
+
 def test_norm_not_finite(rm):
     x = torch.ones(4, 272)
     x[1, 130], x[2, 3] = float("nan"), float("inf")
