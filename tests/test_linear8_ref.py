@@ -115,3 +115,13 @@ def test_matmul_refuses(kw, status):
              act=rm.RM_ACT_NONE, out_dtype=rm.RM_BF16)
     a = rm.rm_matmul_fp8_args(**{**d, **kw})
     assert lib.rm_matmul_fp8_block(ctypes.byref(a), None) == getattr(rm, "RM_" + ("OK" if status == "OK" else "ERR_" + status))
+
+
+def test_which_kernel():
+    """The ends of the product's launch rule: few rows at any size, large products on the CTA pairs."""
+    from linear8_route import few_rows
+    rm, _ = _lib()
+    assert few_rows(rm, 1, 1, 16, 16, "bf16") and few_rows(rm, 32, 32, 6144, 1536, "e4m3", "tanh")
+    assert few_rows(rm, 1, 64, 1024, 16384, "bf16")
+    for out in ("bf16", "f32", "e4m3"):
+        assert not few_rows(rm, 32, 512, 6144, 1536, out) and not few_rows(rm, 1, 8192, 8192, 8192, out, "erf")

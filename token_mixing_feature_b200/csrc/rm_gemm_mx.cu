@@ -668,19 +668,7 @@ cudaError_t launch_out(const rm_matmul_fp8_args& a, MxParams& p, int num_sms, cu
 
 }  // namespace
 
-cudaError_t launch_gemm_mx(const rm_matmul_fp8_args& a, int num_sms, cudaStream_t s) {
-    MxParams p{};
-    p.G = a.G, p.M = a.M, p.N = a.N, p.K = a.K;
-    p.a_scale = a.a_scale, p.as_gs = a.as_gstride, p.as_ld = a.as_ld;
-    p.w_scale = a.w_scale, p.ws_gs = a.ws_gstride, p.ws_ld = a.ws_ld;
-    p.w_shift = a.w_block_rows == 128 ? 7 : 0;
-    p.bias = a.bias;
-    p.resid = a.resid, p.r_gs = a.r_gstride, p.r_ld = a.r_ld;
-    p.o_gs = a.o_gstride, p.o_ld = a.o_ld;
-    p.out_scale = a.out_scale, p.os_gs = a.os_gstride, p.os_ld = a.os_ld;
-    p.act = a.act;
-    p.err = DeviceErr{a.device_status, nullptr};
-    p.budget_ns = a.wait_budget_ns ? a.wait_budget_ns : 1000000000ull;
+bool gemm_mx_few_rows(const rm_matmul_fp8_args& a, int num_sms) {
     // Few rows, or at most one 64 x 128 tile an SM: the few-row kernel, which
     // starts more CTAs and splits K.  Measured, pair / few in us: M 64, N = K = 4096
     // 13.8 / 8.4; M 64, N 1024, K 16384 40.2 / 10.1; 8 groups, M 128, N 1024 (128
@@ -699,7 +687,23 @@ cudaError_t launch_gemm_mx(const rm_matmul_fp8_args& a, int num_sms, cudaStream_
     const long long tiles = (long long)a.G * ((a.M + 63) / 64) * ((a.N + 127) / 128);
     const bool finish = a.out_dtype != RM_BF16 || a.act == RM_ACT_GELU_TANH || a.act == RM_ACT_GELU_ERF;
     const bool one_wave = tiles <= (finish && a.K <= 2048 ? 2 : 1) * num_sms;
-    if (a.M <= 32 || one_wave) return launch_gemm_mx_few(a, p, num_sms, s);
+    return a.M <= 32 || one_wave;
+}
+
+cudaError_t launch_gemm_mx(const rm_matmul_fp8_args& a, int num_sms, cudaStream_t s) {
+    MxParams p{};
+    p.G = a.G, p.M = a.M, p.N = a.N, p.K = a.K;
+    p.a_scale = a.a_scale, p.as_gs = a.as_gstride, p.as_ld = a.as_ld;
+    p.w_scale = a.w_scale, p.ws_gs = a.ws_gstride, p.ws_ld = a.ws_ld;
+    p.w_shift = a.w_block_rows == 128 ? 7 : 0;
+    p.bias = a.bias;
+    p.resid = a.resid, p.r_gs = a.r_gstride, p.r_ld = a.r_ld;
+    p.o_gs = a.o_gstride, p.o_ld = a.o_ld;
+    p.out_scale = a.out_scale, p.os_gs = a.os_gstride, p.os_ld = a.os_ld;
+    p.act = a.act;
+    p.err = DeviceErr{a.device_status, nullptr};
+    p.budget_ns = a.wait_budget_ns ? a.wait_budget_ns : 1000000000ull;
+    if (gemm_mx_few_rows(a, num_sms)) return launch_gemm_mx_few(a, p, num_sms, s);
     switch (a.out_dtype) {
         case RM_F32: return launch_out<RM_F32>(a, p, num_sms, s);
         case RM_BF16: return launch_out<RM_BF16>(a, p, num_sms, s);

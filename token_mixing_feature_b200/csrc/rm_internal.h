@@ -266,5 +266,11 @@ struct QuantBlock {
 cudaError_t launch_quant_block(int dtype, const QuantBlock& p, int block_rows, cudaStream_t s);
 // out = act(A W^T + bias) + resid, group by group, on block-scaled operands.
 cudaError_t launch_gemm_mx(const rm_matmul_fp8_args& a, int num_sms, cudaStream_t s);
+// Whether that product goes to the few-row kernel (else to the CTA pairs).
+bool gemm_mx_few_rows(const rm_matmul_fp8_args& a, int num_sms);
 
 }  // namespace rm
+
+// The same for the tests, which name the kernel that a shape is meant for.  Not
+// part of the library's interface.
+extern "C" int rm_internal_matmul_fp8_few_rows(const rm_matmul_fp8_args* a, int num_sms);

@@ -156,4 +156,8 @@ rm_status rm_matmul_fp8_block(const rm_matmul_fp8_args* a, rm_stream_t stream) {
     return cuda_status(rm::launch_gemm_mx(*a, sms, stream));
 }
 
+int rm_internal_matmul_fp8_few_rows(const rm_matmul_fp8_args* a, int num_sms) {
+    return rm::gemm_mx_few_rows(*a, num_sms) ? 1 : 0;
+}
+
 }  // extern "C"
