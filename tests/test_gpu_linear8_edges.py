@@ -1,0 +1,80 @@
+"""The block-scaled 8-bit linear layer where it can go wrong: small values of GELU, gradients in place, rings of a
+single row, waits that run out.
+
+u = 2^-24 is half a step of fp32 relative to the value.
+"""
+import numpy as np
+import pytest
+import torch
+
+import linear8_ref as R
+from linear8_route import few_rows
+from test_gpu_linear8 import HALF, U, bytes_of, codes_of, gen, h64, rm, rows_of  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32, "e4m3": torch.float8_e4m3fn}
+
+
+# ------------------------------------------------------------------ activations
+def gelu64(v, act):
+    """v sigmoid(2 sqrt(2/pi) (v + 0.044715 v^3)), v Phi(v): forms without cancellation."""
+    from scipy.special import expit, ndtr
+    if act == "tanh":
+        return v * expit(2 * np.sqrt(2 / np.pi) * (v + 0.044715 * v ** 3))
+    return v * ndtr(v)
+
+
+def gelu_slack(v, act):
+    """Errors relative to the result.  tanh: the sigmoid's argument 2 w (w the tanh form's) takes six roundings at most
+    (v^2, three of the cubic coefficient, the sum's fma, the last product), so e^-2w is off by 6 u * 2|w| and its exp2
+    by 4 u (2^-22); 1 + e rounds once, the reciprocal is good to 2 u, the product rounds once: (12 |w| + 8) u.
+    Results below 2^-118 may be flushed to zero."""
+    w = np.abs(np.sqrt(2 / np.pi) * (v + 0.044715 * v ** 3))
+    return (12 * w + 8) * U * np.abs(gelu64(v, act)) + 2.0 ** -118
+
+
+def activated(rm, v, out, act, pairs):
+    """act(v) through the product: operands of zeros, v the bias.  pairs: by the CTA pairs, else by few rows."""
+    M, N = (2600, v.numel()) if pairs else (5, v.numel())
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert few_rows(rm, 1, M, N, 16, out, act, sms) != pairs
+    z = dict(dtype=torch.uint8, device="cuda")
+    A, W = torch.zeros(M, 16, **z), torch.zeros(N, 16, **z)
+    As, Ws = torch.full((M, 1), 127, **z), torch.full(((N + 127) // 128, 1), 127, **z)
+    o = torch.full((M, N), 3, dtype=torch.float32).to(TYPES[out]).cuda()
+    s = torch.empty(M, (N + 127) // 128, **z) if out == "e4m3" else None
+    rm.rm_matmul_fp8_block(A, As, W, Ws, o, s, bias=v.cuda(), act=act)
+    torch.cuda.synchronize()
+    assert torch.equal(o.view(torch.uint8), o[:1].expand(M, N).contiguous().view(torch.uint8))     # every row the same
+    return o[:1], None if s is None else s[:1]
+
+
+SPANS = {"near zero": (-0.02, 0.02), "bulk": (-3.0, 3.0), "left": (-6.0, -2.0), "far left": (-13.5, -6.0), "wide": (-40.0, 40.0)}
+
+
+@pytest.mark.parametrize("act", ["tanh"])
+@pytest.mark.parametrize("out", ["bf16", "f32", "e4m3"])
+@pytest.mark.parametrize("span", SPANS)
+@pytest.mark.parametrize("pairs", [False, True])
+def test_gelu_is_relatively_exact(rm, act, out, span, pairs):
+    """GELU keeps its relative precision where it is small (v = -3: -0.004, v = -5: -2.3e-7)."""
+    v = torch.linspace(*SPANS[span], 1024)
+    ref, slack = gelu64(h64(v), act)[None], gelu_slack(h64(v), act)[None]
+    got, s = activated(rm, v, out, act, pairs)
+    if out == "e4m3":
+        R.assert_quantized(codes_of(got), bytes_of(s), ref, slack, act)
+    else:
+        err = np.abs(h64(got) - ref)
+        assert np.all(err <= slack + HALF[TYPES[out]] * np.abs(ref) * 1.001), f"{np.max(err / np.maximum(np.abs(ref), 1e-37))}"
+
+
+@pytest.mark.parametrize("act", ["tanh", "erf", "relu"])
+@pytest.mark.parametrize("pairs", [False, True])
+def test_activations_of_extremes(rm, act, pairs):
+    """Infinities, NaN and values whose squares leave fp32: the definition's limits."""
+    v = torch.zeros(1024)
+    v[:8] = torch.tensor([float("inf"), 3e38, 1e20, -1e20, -3e38, float("nan"), 0.0, -0.0])
+    for out in ("bf16", "f32"):
+        got = activated(rm, v, out, act, pairs)[0][0].float().cpu()
+        assert got[0] == float("inf") and bool((got[1:3] == v[1:3].to(TYPES[out]).float()).all())
+        assert bool((got[3:5] == 0).all()) and bool(got[5].isnan()) and bool((got[6:] == 0).all())

@@ -87,12 +87,12 @@ __device__ __forceinline__ Tile decode(uint32_t idx, uint32_t mblk, uint32_t nbl
     return Tile{(int)g, (int)(m0 + q - nb * rows) * TM, (int)nb * BN};
 }
 
-template <int OUT, int NV>
+template <int NV>
 __device__ __forceinline__ void activate_all(float (&v)[NV], int act) {
     switch (act) {
-        case RM_ACT_GELU_TANH: activate<RM_ACT_GELU_TANH, OUT != RM_BF16>(v); break;
-        case RM_ACT_GELU_ERF: activate<RM_ACT_GELU_ERF, OUT != RM_BF16>(v); break;
-        case RM_ACT_RELU: activate<RM_ACT_RELU, OUT != RM_BF16>(v); break;
+        case RM_ACT_GELU_TANH: activate<RM_ACT_GELU_TANH>(v); break;
+        case RM_ACT_GELU_ERF: activate<RM_ACT_GELU_ERF>(v); break;
+        case RM_ACT_RELU: activate<RM_ACT_RELU>(v); break;
         default: break;
     }
 }
@@ -124,7 +124,7 @@ __device__ __forceinline__ void finish_row(float (&v)[kChunk], const MxParams& p
             v[4 * q] = lo.x, v[4 * q + 1] = lo.y, v[4 * q + 2] = hi.x, v[4 * q + 3] = hi.y;
         }
     }
-    activate_all<RM_BF16>(v, p.act);
+    activate_all(v, p.act);
 }
 
 // The residual's box in the staging buffer (32 rows x 128 bytes, in the
@@ -171,7 +171,6 @@ __device__ __forceinline__ void load_piece(uint32_t taddr, float* v) {
 }
 
 // bias (128 floats in shared memory) and activation, in place.
-template <int OUT>
 __device__ __forceinline__ void finish_quads(float (&v)[kFrag], const MxParams& p, uint32_t bias, int lane) {
     if (p.bias) {
 #pragma unroll
@@ -184,7 +183,7 @@ __device__ __forceinline__ void finish_quads(float (&v)[kFrag], const MxParams& 
             }
         }
     }
-    activate_all<OUT>(v, p.act);
+    activate_all(v, p.act);
 }
 
 // The scale of each of the thread's two rows (its quad's largest magnitude over
@@ -589,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (h == 1) have_read(tdone0 + 8 * acc);
                     const int r0 = row0 + 16 * h;
                     if (r0 >= p.M || n >= p.N) continue;   // (one value per warp)
-                    if constexpr (!PLAIN) finish_quads<OUT>(v, p, bias_s, lane);
+                    if constexpr (!PLAIN) finish_quads(v, p, bias_s, lane);
                     if constexpr (OUT == RM_F32) {
                         if constexpr (EPI == MX_RESID) {
                             ok = arrived(0, wc, true);

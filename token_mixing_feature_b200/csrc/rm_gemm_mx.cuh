@@ -45,18 +45,16 @@ __device__ __forceinline__ float2 rcp_pair(float2 x) {
     return y;
 }
 
-// act(v) of a pair, without branches.  GELU's tanh form goes through
-// tanh.approx (absolute error 2^-10.9 of tanh) where the result is rounded to
-// bf16; else it is v * sigmoid(2u), u = sqrt(2/pi) (v + 0.044715 v^3) (8-bit
-// results too: the error would move codes across their borders).  The erf form
+// act(v) of a pair, without branches.  GELU's tanh form is v * sigmoid(2u), u =
+// sqrt(2/pi) (v + 0.044715 v^3), which loses nothing where GELU is small, for every
+// type of result: v/2 + v/2 tanh(u) cancels there, and with tanh.approx (2^-11) bf16
+// results were 4.5 % off at v = -4.5 and zero from -5 on.  The erf form
 // takes Abramowitz and Stegun's 7.1.26, erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2),
 // t = 1 / (1 + 0.3275911 x), x >= 0, whose error is at most 1.5e-7, on the side
 // where nothing cancels.
-template <int ACT, bool PRECISE>
+template <int ACT>
 __device__ __forceinline__ float2 activation(float2 v) {
-    if constexpr (ACT == RM_ACT_GELU_TANH && !PRECISE) {
-        return gelu_tanh_pair(v);
-    } else if constexpr (ACT == RM_ACT_GELU_TANH) {
+    if constexpr (ACT == RM_ACT_GELU_TANH) {
         const float c = -2.0f * 0.7978845608028654f * 1.4426950408889634f;   // -2 sqrt(2/pi) log2(e)
         const float2 e = exp2_pair(f2_mul(v, f2_fma(f2_mul(v, v), f2(c * 0.044715f), f2(c))));
         return f2_mul(v, rcp_pair(f2_add(e, f2(1.0f))));
@@ -74,11 +72,11 @@ __device__ __forceinline__ float2 activation(float2 v) {
         return make_float2(v.x < 0.f ? 0.f : v.x, v.y < 0.f ? 0.f : v.y);   // (keeps NaN)
     }
 }
-template <int ACT, bool PRECISE, int NV>
+template <int ACT, int NV>
 __device__ __forceinline__ void activate(float (&v)[NV]) {
 #pragma unroll
     for (int e = 0; e < NV; e += 2) {
-        const float2 y = activation<ACT, PRECISE>(make_float2(v[e], v[e + 1]));
+        const float2 y = activation<ACT>(make_float2(v[e], v[e + 1]));
         v[e] = y.x, v[e + 1] = y.y;
     }
 }

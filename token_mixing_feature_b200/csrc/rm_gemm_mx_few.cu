@@ -59,9 +59,9 @@ __device__ __forceinline__ void put_row(float4 x, const MxParams& p, void* out, 
     const bool in = n < p.N;
     float v[4] = {x.x, x.y, x.z, x.w};
     switch (p.act) {
-        case RM_ACT_GELU_TANH: activate<RM_ACT_GELU_TANH, OUT != RM_BF16>(v); break;
-        case RM_ACT_GELU_ERF: activate<RM_ACT_GELU_ERF, OUT != RM_BF16>(v); break;
-        case RM_ACT_RELU: activate<RM_ACT_RELU, OUT != RM_BF16>(v); break;
+        case RM_ACT_GELU_TANH: activate<RM_ACT_GELU_TANH>(v); break;
+        case RM_ACT_GELU_ERF: activate<RM_ACT_GELU_ERF>(v); break;
+        case RM_ACT_RELU: activate<RM_ACT_RELU>(v); break;
         default: break;
     }
     if constexpr (OUT == RM_E4M3) {
