@@ -49,9 +49,12 @@ __device__ __forceinline__ float2 rcp_pair(float2 x) {
 // sqrt(2/pi) (v + 0.044715 v^3), which loses nothing where GELU is small, for every
 // type of result: v/2 + v/2 tanh(u) cancels there, and with tanh.approx (2^-11) bf16
 // results were 4.5 % off at v = -4.5 and zero from -5 on.  The erf form
-// takes Abramowitz and Stegun's 7.1.26, erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2),
-// t = 1 / (1 + 0.3275911 x), x >= 0, whose error is at most 1.5e-7, on the side
-// where nothing cancels.
+// is v Phi(v), Phi(-a) = erfc(a / sqrt(2)) / 2 = t Q(t) exp(-a^2 / 2) with t = 1 / (1 +
+// a / (2 sqrt(2))) and Q of degree 8, fitted here to erfcx(a / sqrt(2)) / (2 t) with a
+// minimax relative error of 4e-8 (iteratively reweighted least squares over 0 <= a <=
+// 14.8); the exponent is carried in two floats.  All of it is good to 5e-7 of the value
+// down to v = -6, 1.5e-6 to where fp32 ends (v = -13).  (Abramowitz and Stegun's 7.1.26
+// has 1.5e-7 of 1: 5e-5 of the value at v = -3, 2e-3 at -5.)
 template <int ACT>
 __device__ __forceinline__ float2 activation(float2 v) {
     if constexpr (ACT == RM_ACT_GELU_TANH) {
@@ -59,14 +62,26 @@ __device__ __forceinline__ float2 activation(float2 v) {
         const float2 e = exp2_pair(f2_mul(v, f2_fma(f2_mul(v, v), f2(c * 0.044715f), f2(c))));
         return f2_mul(v, rcp_pair(f2_add(e, f2(1.0f))));
     } else if constexpr (ACT == RM_ACT_GELU_ERF) {
-        const float2 x = f2_mul(make_float2(fabsf(v.x), fabsf(v.y)), f2(0.7071067811865476f));
-        const float2 t = rcp_pair(f2_fma(x, f2(0.3275911f), f2(1.0f)));
-        float2 q = f2_fma(t, f2(1.061405429f), f2(-1.453152027f));
-        q = f2_fma(t, q, f2(1.421413741f));
-        q = f2_fma(t, q, f2(-0.284496736f));
-        q = f2_fma(t, q, f2(0.254829592f));
-        const float2 e = exp2_pair(f2_mul(f2_mul(v, v), f2(-0.5f * 1.4426950408889634f)));   // exp(-x^2)
-        const float2 hc = f2_mul(f2_mul(f2_mul(q, t), e), f2(0.5f));   // erfc(x) / 2
+        // (behind 16 Phi(-a) is below fp32: nothing overflows)
+        const float2 a = make_float2(fminf(fabsf(v.x), 16.f), fminf(fabsf(v.y), 16.f));
+        const float2 t = rcp_pair(f2_fma(a, f2(0.35355339059327379f), f2(1.0f)));
+        float2 q = f2(-0.029596666f);
+        q = f2_fma(t, q, f2(0.14259142f));
+        q = f2_fma(t, q, f2(-0.24423045f));
+        q = f2_fma(t, q, f2(0.1397563f));
+        q = f2_fma(t, q, f2(-0.013811729f));
+        q = f2_fma(t, q, f2(0.10155497f));
+        q = f2_fma(t, q, f2(0.12149831f));
+        q = f2_fma(t, q, f2(0.14119503f));
+        q = f2_fma(t, q, f2(0.14104278f));
+        // exp(-a^2 / 2) = exp2(n + r): n the product as it is rounded, r what that
+        // and the constant's own rounding left
+        const float c = -0.5f * 1.4426950408889634f, c_low = -9.629815e-09f;
+        const float2 y = f2_mul(a, a), n = f2_mul(y, f2(c));
+        const float2 minus_y = make_float2(-y.x, -y.y), minus_n = make_float2(-n.x, -n.y);
+        const float2 r = f2_fma(f2_fma(a, a, minus_y), f2(c), f2_fma(y, f2(c_low), f2_fma(y, f2(c), minus_n)));
+        const float2 e = exp2_pair(n);
+        const float2 hc = f2_mul(f2_mul(q, t), f2_fma(f2_mul(r, f2(0.6931471805599453f)), e, e));   // Phi(-a)
         return f2_mul(v, make_float2(v.x < 0.f ? hc.x : 1.0f - hc.x, v.y < 0.f ? hc.y : 1.0f - hc.y));
     } else {
         return make_float2(v.x < 0.f ? 0.f : v.x, v.y < 0.f ? 0.f : v.y);   // (keeps NaN)
