@@ -82,3 +82,59 @@ def test_activations_of_extremes(rm, act, pairs):
         got = activated(rm, v, out, act, pairs)[0][0].float().cpu()
         assert got[0] == float("inf") and bool((got[1:3] == v[1:3].to(TYPES[out]).float()).all())
         assert bool((got[3:5] == 0).all()) and bool(got[5].isnan()) and bool((got[6:] == 0).all())
+
+
+# ------------------------------------------------------------- waits that run out
+def bits(t):
+    return t.contiguous().view(torch.uint8)
+
+
+def run_out(rm, G, M, N, K, out, resid=False, act=None, pairs=False):
+    """Products with wait budgets from 1 ns on: whatever ran out, each element of the results is the right one or what
+    it was, and the status tells if any is missing.  The calls return and later calls are right."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert few_rows(rm, G, M, N, K, out, act, sms) != pairs
+    g = torch.Generator("cuda").manual_seed(K)
+    nb = (K + 127) // 128
+    A, W = (torch.randn(G, n, K, generator=g, device="cuda").to(torch.float8_e4m3fn) for n in (M, N))
+    As, Ws = (torch.full((G, n, nb), 120, dtype=torch.uint8, device="cuda") for n in (M, -(-N // 128)))
+    r = torch.randn(G, M, N, generator=g, device="cuda").to(TYPES[out]) if resid else None
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+
+    def call(budget):
+        o = torch.full((G, M, N), 77, dtype=torch.float32, device="cuda").to(TYPES[out])
+        s = torch.full((G, M, (N + 127) // 128), 77, dtype=torch.uint8, device="cuda") if out == "e4m3" else None
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        flush.fill_(1)      # the operands come from HBM
+        rm.rm_matmul_fp8_block(A, As, W, Ws, o, s, None, act, r, 128, status, budget)
+        torch.cuda.synchronize()
+        return o, s, int(status)
+
+    want, want_s, status = call(0)
+    assert status == rm.RM_OK
+    untouched = torch.full((1,), 77, dtype=torch.float32, device="cuda").to(TYPES[out])
+    missing = []
+    for budget in (1, 1, 500, 2000, 8000):
+        o, s, status = call(budget)
+        assert status in (rm.RM_OK, rm.RM_ERR_DEVICE_TIMEOUT)
+        right = bits(o).view(-1, o.element_size()) == bits(want).view(-1, o.element_size())
+        left = bits(o).view(-1, o.element_size()) == bits(untouched).view(1, -1)
+        assert bool((right.all(1) | left.all(1)).all()), budget
+        if s is not None:
+            assert bool(((s == want_s) | (s == 77)).all()), budget
+        missing.append(int((~right.all(1)).sum()))
+        if status == rm.RM_OK:
+            assert missing[-1] == 0 and (s is None or torch.equal(s, want_s))
+        if budget == 1:
+            assert status == rm.RM_ERR_DEVICE_TIMEOUT
+    again, again_s, status = call(0)
+    assert status == rm.RM_OK and torch.equal(bits(again), bits(want))
+    assert again_s is None or torch.equal(again_s, want_s)
+    print(missing, "of", want.numel())
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32", "e4m3"])
+@pytest.mark.parametrize("G,M,N,K", [(1, 64, 1024, 16384), (1, 20, 2048, 4096), (1, 5, 9472, 8192), (32, 4, 2048, 1536)])
+def test_few_row_waits_run_out(rm, G, M, N, K, out):
+    """K split over clusters of 8, 8 and 4 CTAs and not at all: a tile of which one slice gave up is not stored."""
+    run_out(rm, G, M, N, K, out, resid=out == "f32")

@@ -102,6 +102,10 @@ __device__ __forceinline__ WaitCtx drain_ctx(const WaitCtx& w) {
     return WaitCtx{w.abort, w.budget_ns > 1000000000ull ? w.budget_ns : 1000000000ull, w.err};
 }
 
+// A wait of a whole warp: all lanes go on, or none.
+__device__ __forceinline__ bool warp_mx_wait(uint32_t bar, uint32_t parity, const WaitCtx& w, int site) {
+    return __all_sync(0xffffffffu, mx_wait(bar, parity, w, site));
+}
 // A wait of a whole warp: all lanes go on, or none.  CLUSTER: for what the
 // pair's other CTA released.
 template <bool CLUSTER = false>

@@ -49,6 +49,9 @@ struct Cfg {
 __device__ __forceinline__ void st_cluster_f32(uint32_t a, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
+__device__ __forceinline__ void st_cluster_u32(uint32_t a, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
@@ -123,6 +126,7 @@ __global__ void __launch_bounds__(kThreads)
     const uint32_t done_bar = sempty0 + 8 * kSlots;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* failed = abort_flag + 1;   // a slice of this tile gave up
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slice = (int)(blockIdx.x & (slices - 1));   // = the CTA's rank in its cluster
@@ -136,7 +140,7 @@ __global__ void __launch_bounds__(kThreads)
             mbar_init(sempty0 + 8 * s, 1);
         }
         mbar_init(done_bar, 1);
-        *abort_flag = 0;
+        *abort_flag = *failed = 0;
         fence_mbar_init();
         prefetch_tmap(&tmA);
         prefetch_tmap(&tmW);
@@ -168,7 +172,7 @@ __global__ void __launch_bounds__(kThreads)
         int stage = 0;
         uint32_t phase = 0, issued = 0, issued_phase = 0;
         for (int kb = 0; kb < nkb; ++kb) {
-            if (!warp_wait(empty0 + 8 * stage, phase ^ 1u, wc, SITE_MX_PRODUCER)) break;
+            if (!warp_mx_wait(empty0 + 8 * stage, phase ^ 1u, wc, SITE_MX_PRODUCER)) break;
             if (elect_one()) {
                 const uint32_t fb = full0 + 8 * stage, sa = sbase + stage * C::STAGE_BYTES;
                 mbar_arrive_expect_tx(fb, C::STAGE_BYTES);
@@ -193,10 +197,10 @@ __global__ void __launch_bounds__(kThreads)
             const int c = kb >> 2;
             const bool begin = (kb & 3) == 0, end = (kb & 3) == 3 || kb == nkb - 1;
             const int old = c - kTSlots;   // its MMAs read the tensor memory that chunk c's scales go to
-            if ((begin && (!warp_wait(sfull0 + 8 * (c % kSlots), (uint32_t)(c / kSlots) & 1u, wc, SITE_MX_SCALES) ||
+            if ((begin && (!warp_mx_wait(sfull0 + 8 * (c % kSlots), (uint32_t)(c / kSlots) & 1u, wc, SITE_MX_SCALES) ||
                            (old >= 0 &&
-                            !warp_wait(sempty0 + 8 * (old % kSlots), (uint32_t)(old / kSlots) & 1u, wc, SITE_MX_SCALES)))) ||
-                !warp_wait(full0 + 8 * stage, phase, wc, SITE_MX_MMA))
+                            !warp_mx_wait(sempty0 + 8 * (old % kSlots), (uint32_t)(old / kSlots) & 1u, wc, SITE_MX_SCALES)))) ||
+                !warp_mx_wait(full0 + 8 * stage, phase, wc, SITE_MX_MMA))
                 break;
             tc_fence_after();
             if (elect_one()) {
@@ -227,7 +231,7 @@ __global__ void __launch_bounds__(kThreads)
         const int rows = warp == 2 ? p.N : min(p.M, m0 + NB);
         for (int c = 0; c < chunks; ++c) {
             const uint4 w = atom_words(s + kb0, ld, shift, r0, rows, lane, c, nkb);
-            if (!warp_wait(sempty0 + 8 * (c % kSlots), ((uint32_t)(c / kSlots) & 1u) ^ 1u, wc, SITE_MX_SCALES)) break;
+            if (!warp_mx_wait(sempty0 + 8 * (c % kSlots), ((uint32_t)(c / kSlots) & 1u) ^ 1u, wc, SITE_MX_SCALES)) break;
             sts128(slot0 + c % kSlots * C::SLOT_BYTES + (warp == 2 ? 0 : 512) + 16 * lane, w);
             fence_proxy_async_shared();
             __syncwarp();
@@ -243,12 +247,14 @@ __global__ void __launch_bounds__(kThreads)
     // of A.  Row r belongs to slice r % slices, which keeps what slice s sends of
     // its i-th row as row s * own + i of its partial results.
     const bool drained = mbar_wait(done_bar, 0, drain, SITE_MX_EPILOGUE, false);
-    const bool ok = __all_sync(0xffffffffu, drained && *abort_flag == 0);
+    const bool ok = __all_sync(0xffffffffu, drained && *abort_flag == 0);   // this slice's sums are complete
     tc_fence_after();
     const int rows = min(NB, p.M - m0);
     const int own = NB >> log_slices;
     if (slices > 1) cluster_wait();
-    if (ok) {
+    if (!ok) {   // (a wait ran out) no CTA of the cluster may store rows that lack this slice
+        if (lane < slices) st_cluster_u32(mapa_shared(smem_u32(tmem_slot + 2), lane), 1u);
+    } else {
         const uint32_t at0 = part0 + 4 * (slice * own * kRowF + warp * 32 + lane);
 #pragma unroll 1
         for (int c = 0; c < rows; c += 16) {
@@ -275,7 +281,7 @@ __global__ void __launch_bounds__(kThreads)
         tc_fence_after();
         tmem_dealloc(tmem, C::TMEM_COLS);
     }
-    if (ok) {
+    if (*failed == 0) {
         const float4* part = reinterpret_cast<const float4*>(smem + (part0 - sbase)) + lane;
         const int last = (rows - 1 - slice) >> log_slices;   // this slice's last row
         for (int i = warp; i <= last; i += 16) {             // four rows of each warp's at a time

@@ -159,6 +159,31 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
+// mbar_wait that keeps to short budgets too: it polls for those.  (A thread that
+// parks on the barrier comes back when the hardware likes, whatever its hint, so no
+// wait for less than some 10 us could run out.)
+__device__ __forceinline__ bool mx_wait(uint32_t bar, uint32_t parity, const WaitCtx& w, int site, bool honour_abort = true) {
+    if (w.budget_ns >= 20000u) return mbar_wait(bar, parity, w, site, honour_abort);
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if (honour_abort && *w.abort) return false;
+        if (globaltimer_ns() - t0 > w.budget_ns) {
+            record_error(w.err, RM_ERR_DEVICE_TIMEOUT, site);
+            *w.abort = 1;
+            return false;
+        }
+    }
+}
+
 // mbar_wait for a phase that the other CTA of the pair has arrived on with
 // release at cluster scope (its scale atoms in its own shared memory).
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, const WaitCtx& w, int site) {
