@@ -384,7 +384,7 @@ rm_status rm_quantize_fp8_block(const rm_quant_block_args *args, rm_stream_t str
  * transposed weight squares as W, and dW = dOut^T A with both operands
  * quantised by rm_quantize_fp8_block's transposed form (w_block_rows 1).
  * wait_budget_ns bounds every device-side wait for work to be done (0: one
- * second); waits that only let copies and tensor-core work in flight come to
+ * second; below some 20 us it is kept to roughly); waits that only let copies and tensor-core work in flight come to
  * their end go on for a second at the least.  device_status (device pointer to an
  * int that holds RM_OK, may be NULL) becomes RM_ERR_DEVICE_TIMEOUT if a wait runs
  * out.  Then each element of out and byte of out_scale either has its result or is

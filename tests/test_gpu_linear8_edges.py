@@ -138,3 +138,10 @@ def run_out(rm, G, M, N, K, out, resid=False, act=None, pairs=False):
 def test_few_row_waits_run_out(rm, G, M, N, K, out):
     """K split over clusters of 8, 8 and 4 CTAs and not at all: a tile of which one slice gave up is not stored."""
     run_out(rm, G, M, N, K, out, resid=out == "f32")
+
+
+@pytest.mark.parametrize("out,resid", [("bf16", False), ("f32", False), ("e4m3", False), ("bf16", True), ("f32", True)])
+@pytest.mark.parametrize("G,M,N,K", [(2, 1300, 1168, 1536), (1, 2560, 2576, 4096), (5, 800, 1008, 272), (1, 2600, 1040, 16)])
+def test_pair_waits_run_out(rm, G, M, N, K, out, resid):
+    """The two CTAs of a pair give up apart, their producers up to a ring's length from each other."""
+    run_out(rm, G, M, N, K, out, resid, None if resid else "relu", pairs=True)

@@ -248,6 +248,40 @@ __device__ __forceinline__ void stage_quads_f32(const float (&v)[kFrag], uint32_
             sts64(quad_at(buf, i, h, lane), make_uint2(__float_as_uint(v[4 * i + 2 * h]), __float_as_uint(v[4 * i + 2 * h + 1])));
 }
 
+// What a CTA's producer has issued: the stage and phase that come next, and the
+// number of stages so far (its last four bits, and whether it is 8 or more; the
+// producer counts on from 16 behind 31).
+__device__ __forceinline__ uint32_t producer_state(int stage, uint32_t phase, uint32_t count) {
+    return (uint32_t)stage | phase << 3 | (count & 15u) << 4 | (count > 7u ? 1u : 0u) << 8;
+}
+constexpr uint32_t kGaveUp = 1u << 9;   // beside it: a wait of the CTA ran out
+
+// After a wait ran out, on the even CTA (one thread): every copy that either
+// producer has issued lands before the pair's shared memory goes away.  Both count
+// their bytes on this CTA's full barriers, 2 * BYTES a stage, which it arms.  The
+// producers may have stopped a few stages apart: what only the odd one issued is armed
+// here, what only this one issued gets the odd one's bytes taken off.
+template <int STAGES, uint32_t BYTES>
+__device__ __forceinline__ void drain_pair(uint32_t full0, uint32_t own, uint32_t odd, const WaitCtx& drain) {
+    int stage = (int)(own & 7u);
+    uint32_t phase = own >> 3 & 1u;
+    const int issued = (own >> 8 & 1u) ? STAGES : min((int)(own >> 4 & 15u), STAGES);   // stages that may be in flight
+    int ahead = (int)(((odd >> 4) - (own >> 4)) & 15u);   // the odd one's lead: STAGES at most either way
+    if (ahead > 7) ahead -= 16;
+    for (int i = 0; i < issued; ++i) {   // from the last one back
+        if (--stage < 0) stage = STAGES - 1, phase ^= 1u;
+        if (i < -ahead)
+            asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(full0 + 8 * stage), "r"(BYTES) : "memory");
+        mbar_wait(full0 + 8 * stage, phase, drain, SITE_MX_DRAIN, false);
+    }
+    stage = (int)(own & 7u), phase = own >> 3 & 1u;
+    for (int i = 0; i < ahead; ++i) {
+        mbar_arrive_expect_tx(full0 + 8 * stage, BYTES);
+        mbar_wait(full0 + 8 * stage, phase, drain, SITE_MX_DRAIN, false);
+        if (++stage == STAGES) stage = 0, phase ^= 1u;
+    }
+}
+
 template <int OUT, int EPI>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_mx_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
@@ -266,6 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tfull0 = sempty0 + 8 * kSlots, tdone0 = tfull0 + 16, tover_bar = tdone0 + 16, drain_bar = tover_bar + 8, rbar0 = drain_bar + 8;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile uint32_t* state = tmem_slot + 2;   // at the end: each CTA's producer_state
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -314,14 +349,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
         int stage = 0;
-        uint32_t phase = 0, issued = 0, issued_phase = 0;
+        uint32_t phase = 0, count = 0;
         bool ok = true;
         for (uint32_t idx = unit; idx < total && ok; idx += nunits) {
             const Tile t = decode<OUT>(idx, mblk, nblk);
             const int ar = t.m0 + (int)rank * BM, wr = t.n0 + (int)rank * C::B_ROWS;
             const int ag = t.g * p.a_gmul, wg = t.g * p.w_gmul;
             for (int kb = 0; kb < num_kb; ++kb) {
-                if (!warp_wait(empty0 + 8 * stage, phase ^ 1u, wc, SITE_MX_PRODUCER)) {
+                if (!warp_mx_wait(empty0 + 8 * stage, phase ^ 1u, wc, SITE_MX_PRODUCER)) {
                     ok = false;
                     break;
                 }
@@ -332,14 +367,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_load_3d_pair(sa, &tmA, fbl, kb * BK, p.a_g_inner ? ag : ar, p.a_g_inner ? ar : ag);
                     tma_load_3d_pair(sa + C::A_BYTES, &tmW, fbl, kb * BK, p.w_g_inner ? wg : wr, p.w_g_inner ? wr : wg);
                 }
-                issued |= 1u << stage;
-                issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+                count = count == 31u ? 16u : count + 1u;
                 if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
             }
         }
-        if (leader)   // every issued copy lands before shared memory goes away
-            for (int s = 0; s < C::STAGES; ++s)
-                if (issued & (1u << s)) mbar_wait(full0 + 8 * s, (issued_phase >> s) & 1u, drain, SITE_MX_DRAIN, false);
+        if (lane == 0) state[rank] = producer_state(stage, phase, count);
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
@@ -434,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 // the slot is free once the MMAs that read its last content (and
                 // the tensor memory copy of it) have completed
-                if (!warp_wait(sempty0 + 8 * slot, (uint32_t)(c / kSlots & 1) ^ 1u, wc, SITE_MX_SCALES)) {
+                if (!warp_mx_wait(sempty0 + 8 * slot, (uint32_t)(c / kSlots & 1) ^ 1u, wc, SITE_MX_SCALES)) {
                     ok = false;
                     break;
                 }
@@ -483,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             due |= 1u << b;
         };
         const auto arrived = [&](int b, const WaitCtx& w, bool honour_abort) {
-            const bool ok = __all_sync(0xffffffffu, mbar_wait(rbar + 8 * b, rphase >> b & 1u, w, SITE_MX_EPILOGUE, honour_abort));
+            const bool ok = __all_sync(0xffffffffu, mx_wait(rbar + 8 * b, rphase >> b & 1u, w, SITE_MX_EPILOGUE, honour_abort));
             if (ok) {
                 rphase ^= 1u << b;
                 due &= ~(1u << b);
@@ -511,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fetch(0, OUT == RM_F32 ? n : n + kChunk * half, row0, t.g);
                 if (OUT != RM_F32) fetch(1, n + (kChunk ^ kChunk * half), row0, t.g);
             }
-            if (!warp_wait(tfull0 + 8 * acc, (uint32_t)(it >> 1) & 1u, wc, SITE_MX_EPILOGUE)) break;
+            if (!warp_mx_wait(tfull0 + 8 * acc, (uint32_t)(it >> 1) & 1u, wc, SITE_MX_EPILOGUE)) break;
             tc_fence_after();
             const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * C::ACC1 + col0);
             // the half of the columns that holds the accumulators' overlap: the last 24
@@ -632,7 +664,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0) {
+        const uint32_t mine = state[rank] | (*abort_flag ? kGaveUp : 0u);
+        state[rank] = mine;
+        st_cluster_u32(mapa_shared(smem_u32(tmem_slot + 2 + rank), rank ^ 1u), mine);
+    }
+    __syncwarp();
     cluster_sync_all();   // the peer may still signal this CTA's barriers
+    if ((state[0] | state[1]) & kGaveUp) {   // (else the MMAs have waited for every copy)
+        if (leader && threadIdx.x == 0) drain_pair<C::STAGES, C::STAGE_BYTES>(full0, state[0], state[1], drain);
+        __syncwarp();
+        cluster_sync_all();
+    }
     if (warp == 0) {
         tc_fence_after();
         tmem_dealloc_pair(tmem, C::TMEM_COLS);

@@ -102,15 +102,14 @@ __device__ __forceinline__ WaitCtx drain_ctx(const WaitCtx& w) {
     return WaitCtx{w.abort, w.budget_ns > 1000000000ull ? w.budget_ns : 1000000000ull, w.err};
 }
 
-// A wait of a whole warp: all lanes go on, or none.
-__device__ __forceinline__ bool warp_mx_wait(uint32_t bar, uint32_t parity, const WaitCtx& w, int site) {
-    return __all_sync(0xffffffffu, mx_wait(bar, parity, w, site));
-}
-// A wait of a whole warp: all lanes go on, or none.  CLUSTER: for what the
-// pair's other CTA released.
+// A wait of a whole warp: all lanes go on, or none.  warp_wait parks (CLUSTER: for
+// what the pair's other CTA released), warp_mx_wait polls where the budget is short.
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtx& w, int site) {
     return __all_sync(0xffffffffu, CLUSTER ? mbar_wait_cluster(bar, parity, w, site) : mbar_wait(bar, parity, w, site));
+}
+__device__ __forceinline__ bool warp_mx_wait(uint32_t bar, uint32_t parity, const WaitCtx& w, int site) {
+    return __all_sync(0xffffffffu, mx_wait(bar, parity, w, site));
 }
 
 // Map of [G][rows][cols] elements of esz bytes with a box of `box` rows x 128

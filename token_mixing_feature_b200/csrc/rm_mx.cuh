@@ -161,7 +161,9 @@ __device__ __forceinline__ bool elect_one() {
 
 // mbar_wait that keeps to short budgets too: it polls for those.  (A thread that
 // parks on the barrier comes back when the hardware likes, whatever its hint, so no
-// wait for less than some 10 us could run out.)
+// wait for less than some 10 us could run out.)  The pair's MMA issuer parks all the
+// same: with the poll in its loop 1024 x 4096 x 4096 took 18.6 instead of 16.9 us, and
+// it ends soon after the loaders and epilogues around it have given up.
 __device__ __forceinline__ bool mx_wait(uint32_t bar, uint32_t parity, const WaitCtx& w, int site, bool honour_abort = true) {
     if (w.budget_ns >= 20000u) return mbar_wait(bar, parity, w, site, honour_abort);
     const uint64_t t0 = globaltimer_ns();
@@ -207,6 +209,9 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
     }
 }
 
+__device__ __forceinline__ void st_cluster_u32(uint32_t a, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
 __device__ __forceinline__ float2 lds_f32x2(uint32_t a) {
     float2 v;
     asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
