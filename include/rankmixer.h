@@ -299,7 +299,7 @@ rm_status rm_stack_forward_fp8(rm_handle *h, const rm_block_weights *blocks, con
  *     r = 1 / sqrt(mean(s^2) + eps)
  *     y = s * r * gamma            (gamma NULL: 1)
  * fp32 arithmetic; every output may be NULL, but not all of them:
- *     Sum [rows][D] dtype: s (may be X or R)     Y [rows][D] dtype: y
+ *     Sum [rows][D] dtype: s     Y [rows][D] dtype: y     (each may be X or R)
  *     Yq [rows][D] e4m3 and Ys [rows][ceil(D/128)] scale bytes (both or
  *     neither): y quantised from fp32 in blocks of 128 along the row
  *     rstd [rows] float: r, which the gradient wants.

@@ -145,3 +145,87 @@ def test_few_row_waits_run_out(rm, G, M, N, K, out):
 def test_pair_waits_run_out(rm, G, M, N, K, out, resid):
     """The two CTAs of a pair give up apart, their producers up to a ring's length from each other."""
     run_out(rm, G, M, N, K, out, resid, None if resid else "relu", pairs=True)
+
+
+# ------------------------------------------------------------- norm: rings, aliases
+def check_norm(rm, rows, D, dtype, resid):
+    """Forward over rows that leave the ring room for one or two of them; bounds of test_gpu_linear8.py."""
+    g = gen(rows + D)
+    x = (torch.randn(rows, D, generator=g) * torch.exp(torch.randn(rows, 1, generator=g))).to(dtype)
+    r = torch.randn(rows, D, generator=g).to(dtype) if resid else None
+    gamma = 1 + 0.2 * torch.randn(D, generator=g)
+    y, s = torch.empty(rows, D, dtype=dtype, device="cuda"), torch.empty(rows, D, dtype=dtype, device="cuda") if resid else None
+    q = torch.empty(rows, D, dtype=torch.uint8, device="cuda")
+    qs, rstd = torch.empty(rows, (D + 127) // 128, dtype=torch.uint8, device="cuda"), torch.empty(rows, device="cuda")
+    rm.rm_rmsnorm_forward(x.cuda(), r.cuda() if resid else None, gamma.cuda(), s, y, q, qs, rstd, 1e-6)
+    torch.cuda.synchronize()
+    st = (x.float() + r.float()).to(dtype) if resid else x
+    if resid:
+        assert torch.equal(s.cpu(), st)
+    ref, rr = R.rmsnorm(h64(st), h64(gamma), 1e-6)
+    assert np.all(np.abs(h64(rstd) - rr) <= 30 * U * rr)
+    assert np.all(np.abs(h64(y) - ref) <= (32 * U + HALF[dtype]) * np.abs(ref))
+    R.assert_quantized(codes_of(q), bytes_of(qs), ref, 32 * U * np.abs(ref), "norm")
+
+
+@pytest.mark.parametrize("D", [8192, 11344, 11360, 11376, 12288, 14208, 14224, 16384])
+@pytest.mark.parametrize("resid", [False, True])
+def test_norm_wide_rows(rm, D, resid):
+    """Several rows a CTA around the widths where gamma and the ring's second row no longer fit together."""
+    check_norm(rm, 400, D, torch.float32, resid)
+
+
+def check_grad(rm, rows, D, dtype, dsum, gamma=True, alias=None):
+    """dX and dgamma against 64 bits (bounds of test_gpu_linear8.py); alias: dX written over dY or dSum."""
+    g = gen(rows + D)
+    s, dy = (torch.randn(rows, D, generator=g).to(dtype) for _ in range(2))
+    ds = torch.randn(rows, D, generator=g).to(dtype) if dsum else None
+    gam = 1 + 0.2 * torch.randn(D, generator=g) if gamma else None
+    rstd = (1 / torch.sqrt(s.double().square().mean(1) + 1e-6)).float()
+    dyd, dsd = dy.cuda(), ds.cuda() if dsum else None
+    dx = {None: torch.empty(rows, D, dtype=dtype, device="cuda"), "dy": dyd, "dsum": dsd}[alias]
+    dg = torch.full((D,), 5.0, device="cuda")
+    ws = torch.empty(rm.rm_rmsnorm_backward_workspace_bytes(rows, D) // 4, device="cuda")
+    rm.rm_rmsnorm_backward(dyd, s.cuda(), gam.cuda() if gamma else None, rstd.cuda(), dsd, dx, dg, ws)
+    torch.cuda.synchronize()
+    S, DY, RS = h64(s), h64(dy), h64(rstd)
+    G, DS = h64(gam) if gamma else np.ones(D), h64(ds) if dsum else 0.0
+    rx, rg = R.rmsnorm_grad(DY, S, G, RS, DS)
+    r = RS[:, None]
+    terms = r * (np.abs(DY * G) + np.abs(S) * r ** 2 * np.abs(DY * G * S).mean(1, keepdims=True)) + np.abs(DS)
+    assert np.all(np.abs(h64(dx) - rx) <= 64 * U * terms + HALF[dtype] * np.abs(rx) * 1.001)
+    assert np.all(np.abs(h64(dg) - rg) <= (rows + 64) * U * np.abs(DY * S * r).sum(0))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dsum", [False, True])
+@pytest.mark.parametrize("D", [8192, 9472, 12288, 14224, 16384])
+def test_norm_grad_one_row_rings(rm, D, dsum, dtype):
+    """Several wide rows a CTA: fp32 with dSum from 8192 on has a single row at a time in the ring."""
+    check_grad(rm, 400, D, dtype, dsum)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,D", [(1, 16), (333, 272), (3001, 256), (400, 16384)])
+@pytest.mark.parametrize("alias,gamma", [("dy", True), ("dsum", True), ("dsum", False), (None, False)])
+def test_norm_grad_in_place(rm, rows, D, dtype, alias, gamma):
+    """dX in the place of dY or dSum, gamma left out."""
+    check_grad(rm, rows, D, dtype, True, gamma, alias)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,D", [(1, 16), (333, 272), (3001, 256), (700, 4112), (400, 16384)])
+def test_norm_in_place(rm, rows, D, dtype):
+    """Y in the place of X, Sum in that of R: the bits of separate outputs."""
+    g = gen(rows + D)
+    x, r = (torch.randn(rows, D, generator=g).to(dtype).cuda() for _ in range(2))
+    gamma = (1 + 0.2 * torch.randn(D, generator=g)).cuda()
+    y, s, xi, ri = torch.empty_like(x), torch.empty_like(x), x.clone(), r.clone()
+    rm.rm_rmsnorm_forward(x, r, gamma, s, y)
+    rm.rm_rmsnorm_forward(xi, ri, gamma, ri, xi)
+    torch.cuda.synchronize()
+    assert torch.equal(xi, y) and torch.equal(ri, s)
+    rm.rm_rmsnorm_forward(x, gamma=gamma, Y=y)
+    rm.rm_rmsnorm_forward(x, gamma=gamma, Y=x)
+    torch.cuda.synchronize()
+    assert torch.equal(x, y)

@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(1024) colsum_parts_kernel(const float* part, f
 struct Shape {
     int nc, warps, groups, threads, stages, grid, gamma_bytes;
     size_t smem;
-    Shape(long long rows, int D, int esz, int inputs, bool gamma, int aim, int short_ctas) {
+    Shape(long long rows, int D, int esz, int inputs, bool gamma, bool gradient, int aim, int short_ctas) {
         const int most = (D * esz / 16 + 31) / 32;
         const size_t row_bytes = (size_t)D * esz * inputs;
         // Groups: as many as there are warps for with `aim` chunks a thread (what
@@ -408,8 +408,14 @@ struct Shape {
         // two rows a group in the ring, one at least
         const auto fit = [&](size_t room) { return (int)std::max<size_t>(1, std::min<size_t>(groups, room / (2 * row_bytes))); };
         const int with = 4 * D + row_bytes <= kRing ? fit(kRing - 4 * D) : 0, without = fit(kRing);
-        // gamma in shared memory where several rows use it and no group gives way
-        gamma_bytes = gamma && rows > 2 * kSms && with == without ? 4 * D : 0;
+        // gamma in shared memory where several rows use it, no group gives way and, in
+        // the forward kernel, the groups keep a second row in the ring if they had one
+        // (3000 x 12288 fp32 with residual: 74.6 us, with gamma in its place 86.0).  The
+        // gradient, which reads gamma between its copies and its sum, wants it near even
+        // so (4096 x 8192 fp32 with dSum 93.6 us, from L2 106; 3000 x 12288 without 110 / 164).
+        const auto two = [&](int g, size_t room) { return room / (row_bytes * g) >= 2; };
+        const bool fits = with == without && (gradient || two(with, kRing - 4 * D) || !two(without, kRing));
+        gamma_bytes = gamma && rows > 2 * kSms && fits ? 4 * D : 0;
         groups = without;
         // the warps that this leaves go to the rows (gradient of 4099 x 7184 fp32, one
         // group: 8 warps 132 us, 15 85 us; of 160 x 1536 bf16 6.1 / 5.1)
@@ -443,7 +449,7 @@ cudaError_t fwd(const RmsNorm& p, const Shape& sh, cudaStream_t s) {
 }
 template <typename E, bool RESID>
 cudaError_t fwd_e(const RmsNorm& p, cudaStream_t s) {
-    const Shape sh(p.rows, p.D, sizeof(E), RESID ? 2 : 1, p.gamma != nullptr, kFwdChunks<E>, kShortCtas);
+    const Shape sh(p.rows, p.D, sizeof(E), RESID ? 2 : 1, p.gamma != nullptr, false, kFwdChunks<E>, kShortCtas);
     switch (sh.nc) {
         case 1: return fwd<E, 1, RESID>(p, sh, s);
         case 2: return fwd<E, 2, RESID>(p, sh, s);
@@ -465,7 +471,7 @@ cudaError_t bwd(const RmsNormGrad& p, const Shape& sh, cudaStream_t s) {
 
 template <typename E>
 cudaError_t bwd_e(const RmsNormGrad& p, int* parts, cudaStream_t s) {
-    const Shape sh(p.rows, p.D, sizeof(E), p.dSum ? 3 : 2, p.gamma != nullptr, kBwdAim, 1);
+    const Shape sh(p.rows, p.D, sizeof(E), p.dSum ? 3 : 2, p.gamma != nullptr, true, kBwdAim, 1);
     *parts = sh.grid;
     switch (sh.nc) {
         case 1: return bwd<E, 1>(p, sh, s);
