@@ -125,3 +125,10 @@ def test_which_kernel():
     assert few_rows(rm, 1, 64, 1024, 16384, "bf16")
     for out in ("bf16", "f32", "e4m3"):
         assert not few_rows(rm, 32, 512, 6144, 1536, out) and not few_rows(rm, 1, 8192, 8192, 8192, out, "erf")
+    # up to two 64 x 128 tiles an SM: where the epilogue is long and K is not
+    for K in (256, 2048):
+        for out, act in (("f32", None), ("bf16", "tanh"), ("bf16", "erf"), ("e4m3", "tanh"), ("e4m3", "relu")):
+            assert few_rows(rm, 8, 256, 1024, K, out, act) and not few_rows(rm, 5, 320, 1600, K, out, act)
+        for out, act in (("e4m3", None), ("bf16", None), ("bf16", "relu")):
+            assert not few_rows(rm, 8, 256, 1024, K, out, act)
+    assert not few_rows(rm, 8, 256, 1024, 4096, "f32")

@@ -720,14 +720,19 @@ bool gemm_mx_few_rows(const rm_matmul_fp8_args& a, int num_sms) {
     // most the few-row kernel wins at any size (32 groups, N 6144, K 1536: 63.2 /
     // 59.2; at 64 rows 65.6 / 74.3).
     //
-    // Where the epilogue is long (other results than bf16, GELU) and K is not, it
-    // wins as long as its tiles are one wave, two on an SM: 8 groups, M 256, N 1024
-    // (256 tiles), K 1024: fp32 9.9 / 8.4, bf16 with GELU 10.8 / 9.6, e4m3 9.2 / 9.2,
-    // with GELU 11.4 / 9.9; K 256: 8.1 / 6.1, 8.9 / 7.4, 7.3 / 6.8, 9.4 / 7.5; K 2048:
-    // 12.6 / 11.4, 13.4 / 12.7, 11.8 / 12.2, 13.8 / 12.8.  A second wave loses (320
-    // tiles, K 256, bf16: 6.7 / 10.2).
+    // Where the epilogue is long and K is not, it wins as long as its tiles are one
+    // wave, two on an SM.  Measured at 160 to 288 tiles, K 256 to 2048; of 8 groups, M
+    // 256, N 1024 (256 tiles), K 256 / 1024 / 2048: fp32 7.8 / 6.3, 9.8 / 8.7, 12.3 / 11.7
+    // (with residual 10.5 / 8.6, 12.5 / 10.8, 15.0 / 14.0); bf16 with GELU 8.4 / 7.2, 10.4 /
+    // 9.5, 12.8 / 12.6; e4m3 with GELU 9.5 / 7.6, 11.6 / 9.9, 14.0 / 13.0, with ReLU 7.9 /
+    // 7.0, 9.8 / 9.5, 12.4 / 12.4.  Not so for e4m3 without activation (6.8 / 7.0, 8.8 /
+    // 9.3, 11.3 / 12.3), bf16 (5.9 / 6.4, 7.9 / 8.8, 10.4 / 11.8), with ReLU (6.8 / 6.5, 8.8 /
+    // 9.0, 11.2 / 12.0) or residual (7.0 / 8.4, 8.9 / 10.9, 11.4 / 14.0), nor at K 4096
+    // (fp32 17.2 / 17.5, e4m3 with ReLU 17.2 / 18.3).  A second wave loses everywhere (325
+    // tiles, K 256, fp32 8.2 / 11.4).
     const long long tiles = (long long)a.G * ((a.M + 63) / 64) * ((a.N + 127) / 128);
-    const bool finish = a.out_dtype != RM_BF16 || a.act == RM_ACT_GELU_TANH || a.act == RM_ACT_GELU_ERF;
+    const bool gelu = a.act == RM_ACT_GELU_TANH || a.act == RM_ACT_GELU_ERF;
+    const bool finish = gelu || a.out_dtype == RM_F32 || (a.out_dtype == RM_E4M3 && a.act != RM_ACT_NONE);
     const bool one_wave = tiles <= (finish && a.K <= 2048 ? 2 : 1) * num_sms;
     return a.M <= 32 || one_wave;
 }
