@@ -351,7 +351,7 @@ rm_status rm_rmsnorm_backward(const rm_rmsnorm_grad_args *args, rm_stream_t stre
  * block_rows 1: blocks of 1 x 128 along the rows of what is written (of the
  * transpose for dst_t); 128: squares, whose transpose has the same codes and
  * scales.  dst_t_ld >= rows is a multiple of 16, rows itself need not be.
- * cols % 16 == 0, else RM_ERR_UNSUPPORTED. */
+ * cols % 16 == 0, rows and cols at most 2^31 - 256, else RM_ERR_UNSUPPORTED. */
 typedef struct {
     const void *src;
     long long src_gstride, src_ld;

@@ -132,3 +132,13 @@ def test_which_kernel():
         for out, act in (("e4m3", None), ("bf16", None), ("bf16", "relu")):
             assert not few_rows(rm, 8, 256, 1024, K, out, act)
     assert not few_rows(rm, 8, 256, 1024, 4096, "f32")
+
+
+def test_quantize_refuses_widths_next_to_2_to_31():
+    """Tiles are counted in ints: the last 255 widths are refused like the last 255 heights."""
+    rm, lib = _lib()
+    for rows, cols in ((1, 0x7ffffff0), (0x7ffffff0, 16)):
+        a = rm.rm_quant_block_args(src=P, src_gstride=1 << 33, src_ld=cols, dst=P, dst_gstride=1 << 33, dst_ld=cols, scale=P,
+                                   scale_gstride=1 << 30, scale_ld=1 << 24, G=1, rows=rows, cols=cols, block_rows=1,
+                                   dtype=rm.RM_BF16)
+        assert lib.rm_quantize_fp8_block(ctypes.byref(a), None) == rm.RM_ERR_UNSUPPORTED

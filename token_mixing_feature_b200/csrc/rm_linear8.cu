@@ -99,7 +99,7 @@ rm_status rm_quantize_fp8_block(const rm_quant_block_args* a, rm_stream_t stream
         return RM_ERR_INVALID_ARG;
     if (a->block_rows != 1 && a->block_rows != 128) return RM_ERR_INVALID_ARG;
     if (a->cols % 16) return RM_ERR_UNSUPPORTED;
-    if (a->rows > 0x7fffff00 || (double)a->G * blocks(a->rows) * blocks(a->cols) > 2147483647.0)
+    if (a->rows > 0x7fffff00 || a->cols > 0x7fffff00 || (double)a->G * blocks(a->rows) * blocks(a->cols) > 2147483647.0)
         return RM_ERR_UNSUPPORTED;
     if (a->G == 0 || a->rows == 0) return RM_OK;
     if ((!a->dst && !a->dst_t) || (a->dst && !a->scale) || (a->dst_t && !a->scale_t)) return RM_ERR_INVALID_ARG;
