@@ -347,7 +347,7 @@ rm_status rm_rmsnorm_backward(const rm_rmsnorm_grad_args *args, rm_stream_t stre
 /* Block quantiser of G matrices src [rows][cols] (bf16 or float), in one read:
  *     dst [rows][cols] e4m3, scale [ceil(rows/block_rows)][ceil(cols/128)], and / or
  *     dst_t [cols][rows] e4m3, scale_t [ceil(cols/block_rows)][ceil(rows/128)]:
- *     the same of the transpose.
+ *     the same of the transpose (codes and scales of an orientation: both or neither).
  * block_rows 1: blocks of 1 x 128 along the rows of what is written (of the
  * transpose for dst_t); 128: squares, whose transpose has the same codes and
  * scales.  dst_t_ld >= rows is a multiple of 16, rows itself need not be.

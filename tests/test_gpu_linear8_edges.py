@@ -229,3 +229,20 @@ def test_norm_in_place(rm, rows, D, dtype):
     rm.rm_rmsnorm_forward(x, gamma=gamma, Y=x)
     torch.cuda.synchronize()
     assert torch.equal(x, y)
+
+
+# ------------------------------------------------------------------- refusals
+def test_wrapper_refuses_budgets_and_status(rm):
+    z = dict(dtype=torch.uint8, device="cuda")
+    args = (torch.zeros(4, 64, **z), torch.zeros(4, 1, **z), torch.zeros(32, 64, **z), torch.zeros(1, 1, **z),
+            torch.zeros(4, 32, device="cuda"))
+    word = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for kw in (dict(wait_budget_ns=-1), dict(wait_budget_ns=1 << 64), dict(device_status=word),
+               dict(device_status=word[:0]), dict(device_status=word[:1].long()), dict(device_status=word[:1].cpu())):
+        with pytest.raises(rm.RankMixerError) as e:
+            rm.rm_matmul_fp8_block(*args, **kw)
+        assert e.value.status == rm.RM_ERR_INVALID_ARG, kw
+    rm.rm_matmul_fp8_block(*args, device_status=word[:1])
+    rm.rm_matmul_fp8_block(*args, device_status=word[0])
+    torch.cuda.synchronize()
+    assert word.tolist() == [0, 0]

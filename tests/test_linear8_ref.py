@@ -142,3 +142,12 @@ def test_quantize_refuses_widths_next_to_2_to_31():
                                    scale_gstride=1 << 30, scale_ld=1 << 24, G=1, rows=rows, cols=cols, block_rows=1,
                                    dtype=rm.RM_BF16)
         assert lib.rm_quantize_fp8_block(ctypes.byref(a), None) == rm.RM_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("kw", [dict(scale_t=P, scale_t_ld=1), dict(dst=None, dst_t=P, dst_t_ld=16, scale_t=P, scale_t_ld=1)])
+def test_quantize_refuses_scales_alone(kw):
+    rm, lib = _lib()
+    d = dict(src=P, src_gstride=640, src_ld=64, dst=P, dst_gstride=640, dst_ld=64, scale=P, scale_gstride=10, scale_ld=1,
+             G=1, rows=10, cols=64, block_rows=1, dtype=rm.RM_BF16)
+    a = rm.rm_quant_block_args(**{**d, **kw})
+    assert lib.rm_quantize_fp8_block(ctypes.byref(a), None) == rm.RM_ERR_INVALID_ARG

@@ -102,7 +102,9 @@ rm_status rm_quantize_fp8_block(const rm_quant_block_args* a, rm_stream_t stream
     if (a->rows > 0x7fffff00 || a->cols > 0x7fffff00 || (double)a->G * blocks(a->rows) * blocks(a->cols) > 2147483647.0)
         return RM_ERR_UNSUPPORTED;
     if (a->G == 0 || a->rows == 0) return RM_OK;
-    if ((!a->dst && !a->dst_t) || (a->dst && !a->scale) || (a->dst_t && !a->scale_t)) return RM_ERR_INVALID_ARG;
+    if ((!a->dst && !a->dst_t) || (a->dst == nullptr) != (a->scale == nullptr) ||
+        (a->dst_t == nullptr) != (a->scale_t == nullptr))
+        return RM_ERR_INVALID_ARG;
     const int esz = a->dtype == RM_BF16 ? 2 : 4, br = a->block_rows;
     if (!al16(a->src) || !row_stride(a->src_ld, a->rows, a->cols, esz) ||
         !group_stride(a->src_gstride, a->G, esz, true))

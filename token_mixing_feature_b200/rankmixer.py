@@ -640,7 +640,11 @@ def rm_matmul_fp8_block(A, A_scale, W, W_scale, out, out_scale=None, bias=None, 
         if b[1] != N and G > 1:
             _wrong(what, "bias", bias, (rt.f32,), (G, N), dev)
         b = b[0]
+    if not 0 <= wait_budget_ns < 1 << 64:
+        _refuse(what, f"wait_budget_ns is {wait_budget_ns}")
     if device_status is not None:
+        if device_status.numel() != 1:
+            _wrong(what, "device_status", device_status, rt.i32, (1,), dev)
         status = _mat(what, "device_status", device_status.view(1, 1), rt.i32, (1, 1), dev)[0]
     a = rm_matmul_fp8_args(
         *_grp(what, "A", A, rt.codes, shape, dev), *_grp(what, "A_scale", A_scale, rt.scales, (G, M, nb), dev),
