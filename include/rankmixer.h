@@ -298,7 +298,8 @@ rm_status rm_stack_forward_fp8(rm_handle *h, const rm_block_weights *blocks, con
  *     s = X + R rounded to dtype (s = X when R is NULL)
  *     r = 1 / sqrt(mean(s^2) + eps)
  *     y = s * r * gamma            (gamma NULL: 1)
- * fp32 arithmetic; every output may be NULL, but not all of them:
+ * fp32 arithmetic (a row whose squares leave fp32, |s| > 1.8e19, gets r = 0); every
+ * output may be NULL, but not all of them:
  *     Sum [rows][D] dtype: s     Y [rows][D] dtype: y     (each may be X or R)
  *     Yq [rows][D] e4m3 and Ys [rows][ceil(D/128)] scale bytes (both or
  *     neither): y quantised from fp32 in blocks of 128 along the row
@@ -374,7 +375,9 @@ rm_status rm_quantize_fp8_block(const rm_quant_block_args *args, rm_stream_t str
  * A [G][M][K] e4m3 with scales a_scale [G][M][ceil(K/128)];  W [G][N][K] e4m3
  * with w_scale [G][ceil(N/w_block_rows)][ceil(K/128)], w_block_rows 1 or 128.
  * A group stride of 0 shares an input among the groups.  fp32 accumulation in
- * the tensor cores, every block's scales applied there.
+ * the tensor cores, every block's scales applied there (their sums truncate: 1e-6 of
+ * the terms at K 1536).  GELU in both forms keeps its relative precision where it is
+ * small (1e-5 of the value at -5), before the result is rounded to its type.
  * out: out_dtype RM_BF16 or RM_F32 (resid, if given, has the same type and may
  * be out), or RM_E4M3 with out_scale [G][M][ceil(N/128)] and no resid: the next
  * product's operand, quantised from fp32.  bias [G][N] float or NULL; act an

@@ -10,9 +10,9 @@
 // a projection of a few hundred columns still asks for its weights from every
 // SM, without a workspace and with the same bits every time.
 //
-// What bounds it: one row through 1536 x 1536 takes 4.6 us, a launch and three
-// trips through memory; four rows through 32 x 6144 x 1536 52 us, 5.8 TB/s of
-// weights (87 % of the measured copy).
+// What bounds it: one row through 1536 x 1536 takes 4.7 us, a launch and three
+// trips through memory; four rows through 32 x 6144 x 1536 52.5 us in a burst, 5.8 TB/s
+// of weights (88 % of the measured copy), 53.6 in a long run.
 //
 // Four warps: 0 loads W and A (bulk copies), 1 issues the MMAs, 2 and 3 load
 // the scales; then all four carry the epilogue, a warp per row of A.

@@ -19,8 +19,8 @@
 // barrier, and what is in flight (up to 220 KB an SM) depends neither on
 // registers nor on where a group is in its row.  With the rows loaded straight
 // into registers, 16384 x 1536 ran at 4.2-4.6 TB/s whatever the launch shape; now
-// 5.5 TB/s (32 us with residual, sum and 8-bit output), 16384 x 7680 6.2 TB/s, the
-// gradient of 16384 x 1536 4.8 TB/s (42 us, 4 of them the column sums).
+// 5.4 TB/s (33 us with residual, sum and 8-bit output), 16384 x 7680 6.5 TB/s, the
+// gradient of 16384 x 1536 4.75 TB/s (42 us, 4.5 of them the column sums).
 #include <cuda_bf16.h>
 
 #include <algorithm>
